@@ -9,7 +9,10 @@ Raw entry points keep the C names (``fgfp8_quant_act`` ...) and take integers
 (device addresses, sizes, a stream handle).  The tensor helpers
 (``quant_act``, ``quant_weight``, ``gemm``, ``grouped_gemm``) allocate the
 outputs with torch on the input's device and call the raw entry points on the
-current stream.
+current stream.  ``gemm_epilogue``, ``linear_epilogue``, ``route_topk`` and
+``moe_decode`` also check their tensors' types, shapes, layouts and device, and
+run on the device of their first tensor, on its current stream or on the given
+one.
 """
 from __future__ import annotations
 
@@ -45,6 +48,14 @@ SIGNATURES = {
     "fgfp8_masked_gemm": (_INT, [_P, _P, _I64, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _INT, _P]),
     "fgfp8_quant_act_masked": (_INT, [_P, _I64, _P, _I32, _I64, _I64, _P, _P, _I64, _INT, _P]),
     "fgfp8_masked_linear": (_INT, [_P, _I64, _P, _P, _I64, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _INT, _P]),
+    "fgfp8_gemm_epilogue": (_INT, [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _INT, _P, _I64, _P]),
+    "fgfp8_linear_epilogue": (_INT, [_P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _INT, _INT, _P,
+                                     _I64, _P]),
+    "fgfp8_route_topk": (_INT, [_P, _INT, _I64, _P, _I64, _I64, _I64, _INT, _I64, _I64, _INT, ctypes.c_float, _P, _P,
+                                _P]),
+    "fgfp8_moe_workspace_bytes": (_INT, [_I64, _I64, _I64, ctypes.POINTER(_I64)]),
+    "fgfp8_moe_decode": (_INT, [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
+                                _INT, _P]),
     "fgfp8_check_device_status": (_INT, [_P]),
     "fgfp8_gather_cols": (_INT, [_P, _I64, _I64, _I64, _P, _P]),
     "fgfp8_selftest_expired_wait": (_INT, [_P]),
@@ -115,6 +126,11 @@ fgfp8_gemm_swiglu_quant = _raw("fgfp8_gemm_swiglu_quant")
 fgfp8_masked_gemm = _raw("fgfp8_masked_gemm")
 fgfp8_quant_act_masked = _raw("fgfp8_quant_act_masked")
 fgfp8_masked_linear = _raw("fgfp8_masked_linear")
+fgfp8_gemm_epilogue = _raw("fgfp8_gemm_epilogue")
+fgfp8_linear_epilogue = _raw("fgfp8_linear_epilogue")
+fgfp8_route_topk = _raw("fgfp8_route_topk")
+fgfp8_moe_workspace_bytes = _raw("fgfp8_moe_workspace_bytes")
+fgfp8_moe_decode = _raw("fgfp8_moe_decode")
 fgfp8_check_device_status = _raw("fgfp8_check_device_status")
 fgfp8_gather_cols = _raw("fgfp8_gather_cols")
 fgfp8_selftest_expired_wait = _raw("fgfp8_selftest_expired_wait")
@@ -377,6 +393,223 @@ def gemm_swiglu_quant(Xq, Xs, Wq_gu, Ws_gu, Hq=None, Hs=None, ld_h: int | None =
                                    Hq.data_ptr(), Hs.data_ptr(), ld_h, M, I, K, _stream(stream)),
            "fgfp8_gemm_swiglu_quant")
     return Hq, Hs
+
+
+# ---------------------------------------------------------------- epilogue, router, expert layer
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+FUSED_QUANT_TOKENS = 16       # linear_epilogue needs no Xq / Xs up to this many tokens
+MOE_MAX_TOKENS = 64
+
+
+def _need(ok: bool, where: str, message: str, status: int = 1) -> None:
+    if not ok:
+        raise FGFP8Error(status, where, message)
+
+
+def _matrix(t, where: str, name: str, dtype, device) -> int:
+    """Checks a row-major matrix operand; returns its row stride."""
+    _need(t.dtype == dtype and t.dim() == 2 and t.device == device, where,
+          f"{name} must be a {dtype} matrix on {device}")
+    R, C = t.shape
+    if R <= 1:
+        return C                  # the stride of a single row says nothing
+    _need(t.stride(1) == 1 or C <= 1, where, f"{name} must have unit stride along its rows")
+    return t.stride(0)
+
+
+def _dense(t, where: str, name: str, dtype, shape, device) -> None:
+    ok = (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype)
+    _need(ok and tuple(t.shape) == shape and t.is_contiguous() and t.device == device, where,
+          f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+
+
+def _codes_dtypes():
+    import torch
+    return torch.uint8, torch.float8_e4m3fn
+
+
+def _check_weight(Wq, Ws, where, fmt, device, names=("Wq", "Ws"), lead=()):
+    _need(fmt in (SCALE_F32, SCALE_UE8M0), where, "fmt must be SCALE_F32 (0) or SCALE_UE8M0 (1)")
+    shape = tuple(Wq.shape)
+    _need(len(shape) == 2 + len(lead) and shape[-1] % 128 == 0 and shape[-2] % 128 == 0, where,
+          f"{names[0]} must be [{', '.join([*lead, 'N', 'K'])}] with N and K multiples of 128", 2)
+    _dense(Wq, where, names[0], _codes_dtypes(), shape, device)
+    _dense(Ws, where, names[1], _scale_dtype(fmt), shape[:-2] + (shape[-2] // 128, shape[-1] // 128), device)
+
+
+def _run_on(device, stream, where: str, call):
+    """call(stream handle) with `device` current; what it allocates belongs to
+    the stream it launches on."""
+    import torch
+    _need(device.type == "cuda", where, "the tensors must be on a CUDA device")
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+        _need(stream.device == device, where, f"the stream must be on {device}")
+        with torch.cuda.stream(stream):
+            return call(int(stream.cuda_stream))
+
+
+def _epilogue_args(where, M, N, device, bias, act, residual):
+    import torch
+    _need(act in _ACTS if isinstance(act, str) else act in _ACTS.values(), where,
+          f"act must be one of {sorted(_ACTS)} or its code")
+    code = _ACTS[act] if isinstance(act, str) else act
+    bp, bt, rp, ld_r = None, 0, None, N
+    if bias is not None:
+        _dense(bias, where, "bias", (torch.bfloat16, torch.float32), (N,), device)
+        bp, bt = bias.data_ptr(), int(bias.dtype == torch.float32)
+    if residual is not None:
+        ld_r = _matrix(residual, where, "residual", torch.bfloat16, device)
+        _need(tuple(residual.shape) == (M, N), where, f"residual must be [{M}, {N}]", 2)
+        rp = residual.data_ptr()
+    return bp, bt, code, rp, ld_r
+
+
+def gemm_epilogue(Xq, Xs, Wq, Ws, fmt: int, bias=None, act="none", residual=None, Y=None, stream=None):
+    """Y = bf16(act(X W^T + bias) + residual) from the quantized operands
+    (Xq uint8 [M, K], Xs [K/128, ld_s], Wq [N, K], Ws [N/128, K/128]); bias [N]
+    bf16 or fp32, residual bf16 [M, N] with any row stride (it may be Y), act
+    one of none, relu, silu, gelu, gelu_tanh.  Returns Y."""
+    import torch
+    where, dev = "gemm_epilogue", Xq.device
+    _check_weight(Wq, Ws, where, fmt, dev)
+    (M, K), N = Xq.shape, Wq.shape[0]
+    _dense(Xq, where, "Xq", _codes_dtypes(), (M, Wq.shape[1]), dev)
+    _dense(Xs, where, "Xs", _scale_dtype(fmt), (K // 128, Xs.shape[-1]), dev)
+    epi = _epilogue_args(where, M, N, dev, bias, act, residual)
+    if Y is not None:
+        _dense(Y, where, "Y", torch.bfloat16, (M, N), dev)
+
+    def call(s):
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if Y is None else Y
+        _check(fgfp8_gemm_epilogue(Xq.data_ptr(), Xs.data_ptr(), Xs.shape[1], Wq.data_ptr(), Ws.data_ptr(),
+                                   out.data_ptr(), M, N, K, fmt, *epi, s), "fgfp8_gemm_epilogue")
+        return out
+    return _run_on(dev, stream, where, call)
+
+
+def linear_epilogue(X, Wq, Ws, fmt: int, bias=None, act="none", residual=None, Y=None, Xq=None, Xs=None,
+                    ld_s: int | None = None, stream=None):
+    """The W8A8 linear layer with its epilogue, Y = bf16(act(X W^T + bias) +
+    residual), from bf16 X [M, K] (any row stride that is a multiple of 8) and
+    the pre-quantized weight.  Xq / Xs are the quantizer's buffers (allocated
+    here when not given, not needed for M <= FUSED_QUANT_TOKENS); bias, act and
+    residual as in gemm_epilogue.  Returns Y."""
+    import torch
+    where, dev = "linear_epilogue", X.device
+    _check_weight(Wq, Ws, where, fmt, dev)
+    ldx = _matrix(X, where, "X", torch.bfloat16, dev)
+    (M, K), N = X.shape, Wq.shape[0]
+    _need(K == Wq.shape[1], where, f"X has {K} columns, Wq {Wq.shape[1]}", 2)
+    epi = _epilogue_args(where, M, N, dev, bias, act, residual)
+    if Y is not None:
+        _dense(Y, where, "Y", torch.bfloat16, (M, N), dev)
+    if Xq is not None:
+        _dense(Xq, where, "Xq", _codes_dtypes(), (M, K), dev)
+    ld = scale_rows(M, fmt) if ld_s is None else ld_s
+    if Xs is not None:
+        _dense(Xs, where, "Xs", _scale_dtype(fmt), (K // 128, ld), dev)
+
+    def call(s):
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if Y is None else Y
+        q, sc = Xq, Xs
+        if M > FUSED_QUANT_TOKENS:
+            if q is None:
+                q = torch.empty((M, K), dtype=torch.uint8, device=dev)
+            if sc is None:
+                sc = torch.empty((K // 128, ld), dtype=_scale_dtype(fmt), device=dev)
+        _check(fgfp8_linear_epilogue(X.data_ptr(), ldx, None if q is None else q.data_ptr(),
+                                     None if sc is None else sc.data_ptr(), ld, Wq.data_ptr(), Ws.data_ptr(),
+                                     out.data_ptr(), M, N, K, fmt, *epi, s), "fgfp8_linear_epilogue")
+        return out
+    return _run_on(dev, stream, where, call)
+
+
+def route_topk(logits, topk: int, score: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
+               renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """Each token's topk experts and their weights from the scores [T, E] (bf16
+    or fp32, any row stride): softmax, or sigmoid with an optional fp32
+    selection bias [E]; the topk_group best of n_group groups compete.
+    Experts at -inf or NaN are never chosen; empty slots hold id -1 and
+    weight 0.  Returns (ids int32 [T, topk], weights fp32 [T, topk])."""
+    import torch
+    where, dev = "route_topk", logits.device
+    _need(logits.dtype in (torch.bfloat16, torch.float32), where, "logits must be bf16 or fp32")
+    ld = _matrix(logits, where, "logits", logits.dtype, dev)
+    T, E = logits.shape
+    _need(score in _SCORES, where, f"score must be one of {sorted(_SCORES)}")
+    if bias is not None:
+        _dense(bias, where, "bias", torch.float32, (E,), dev)
+    if ids is not None:
+        _dense(ids, where, "ids", torch.int32, (T, topk), dev)
+    if weights is not None:
+        _dense(weights, where, "weights", torch.float32, (T, topk), dev)
+    _need(topk >= 1, where, "topk must be at least 1", 2)
+
+    def call(s):
+        i = torch.empty((T, topk), dtype=torch.int32, device=dev) if ids is None else ids
+        w = torch.empty((T, topk), dtype=torch.float32, device=dev) if weights is None else weights
+        _check(fgfp8_route_topk(logits.data_ptr(), int(logits.dtype == torch.float32), ld,
+                                None if bias is None else bias.data_ptr(), T, E, topk, _SCORES[score], n_group,
+                                topk_group, int(renormalize), scale, i.data_ptr(), w.data_ptr(), s),
+               "fgfp8_route_topk")
+        return i, w
+    return _run_on(dev, stream, where, call)
+
+
+def moe_workspace_bytes(T: int, topk: int, I: int) -> int:
+    """Bytes of moe_decode's workspace."""
+    n = ctypes.c_int64()
+    _check(fgfp8_moe_workspace_bytes(T, topk, I, ctypes.byref(n)), "fgfp8_moe_workspace_bytes")
+    return n.value
+
+
+def moe_decode(X, ids, weights, W13q, W13s, W2q, W2s, fmt: int, residual=None, Y=None, workspace=None, stream=None):
+    """A whole SwiGLU expert layer for at most MOE_MAX_TOKENS tokens: X bf16
+    [T, K], ids int32 [T, topk] (negative: empty slot) and weights fp32
+    [T, topk] as from route_topk, W13q [E, 2I, K] / W13s with gate and up
+    interleaved (interleave_gate_up per expert), W2q [E, K, I] / W2s.
+    Y[t] = bf16(residual[t] + sum_j weights[t, j] expert_{ids[t, j]}(X[t])).
+    workspace: uint8 tensor of moe_workspace_bytes(T, topk, I) (allocated here
+    when not given; calls that may overlap need their own).  Returns Y."""
+    import torch
+    where, dev = "moe_decode", X.device
+    _check_weight(W13q, W13s, where, fmt, dev, ("W13q", "W13s"), ("E",))
+    _check_weight(W2q, W2s, where, fmt, dev, ("W2q", "W2s"), ("E",))
+    ldx = _matrix(X, where, "X", torch.bfloat16, dev)
+    T, K = X.shape
+    E, I = W13q.shape[0], W2q.shape[2]
+    _need(tuple(W13q.shape) == (E, 2 * I, K) and tuple(W2q.shape) == (E, K, I), where,
+          "W13q must be [E, 2I, K] and W2q [E, K, I] with X [T, K]", 2)
+    _need(ids.dim() == 2, where, "ids must be [T, topk]", 2)
+    topk = ids.shape[1]
+    _dense(ids, where, "ids", torch.int32, (T, topk), dev)
+    _dense(weights, where, "weights", torch.float32, (T, topk), dev)
+    rp, ld_r = None, K
+    if residual is not None:
+        ld_r = _matrix(residual, where, "residual", torch.bfloat16, dev)
+        _need(tuple(residual.shape) == (T, K), where, f"residual must be [{T}, {K}]", 2)
+        rp = residual.data_ptr()
+    if Y is not None:
+        _dense(Y, where, "Y", torch.bfloat16, (T, K), dev)
+    if workspace is not None:
+        _dense(workspace, where, "workspace", torch.uint8, (workspace.numel(),), dev)
+
+    def call(s):
+        out = torch.empty((T, K), dtype=torch.bfloat16, device=dev) if Y is None else Y
+        ws = workspace
+        if ws is None:
+            ws = torch.empty((moe_workspace_bytes(T, topk, I),), dtype=torch.uint8, device=dev)
+        _check(fgfp8_moe_decode(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), W13q.data_ptr(),
+                                W13s.data_ptr(), W2q.data_ptr(), W2s.data_ptr(), rp, ld_r, out.data_ptr(),
+                                ws.data_ptr(), ws.numel(), T, topk, E, K, I, fmt, s), "fgfp8_moe_decode")
+        return out
+    return _run_on(dev, stream, where, call)
 
 
 def selftest_expired_wait(stream=None) -> None:

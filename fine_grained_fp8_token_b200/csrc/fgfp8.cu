@@ -16,10 +16,12 @@
 #include <string>
 
 #include "fgfp8.h"
+#include "few.cuh"
 #include "gemm.cuh"
 #include "layout.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
+#include "route.cuh"
 
 namespace {
 
@@ -208,12 +210,13 @@ int dense_group_m(int64_t M, int64_t K, int bm) {
 
 // Launch one GEMM instantiation as a persistent grid (one CTA per SM at most).
 // kFuse: the SwiGLU gate/up projection writing the down projection's
-// quantized input (Hq, Hs, ld_h) instead of Y.
-template <int BN, int CW, int FMT, bool kGrouped, bool kFuse = false>
+// quantized input (Hq, Hs, ld_h) instead of Y.  kEpi: bias, activation and
+// residual (epi) before the rounding to bf16.
+template <int BN, int CW, int FMT, bool kGrouped, bool kFuse = false, bool kEpi = false>
 fgfp8_status launch_gemm(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq, const void* Ws,
                          void* Y, int64_t M, int64_t N, int64_t K, const int32_t* offs, int E, int64_t b_rows,
                          cudaStream_t stream, int dev, int sm_count, int early, int cap = 0, uint8_t* Hq = nullptr,
-                         float* Hs = nullptr, int64_t ld_h = 0, int withhold_kb = -1) {
+                         float* Hs = nullptr, int64_t ld_h = 0, int withhold_kb = -1, const fgfp8::EpiArgs& epi = {}) {
   using C = fgfp8::GemmCfg<BN, CW>;
   CUtensorMap mA, mB, mBh;
   fgfp8_status st = make_map_u8_sw128(&mA, Xq, static_cast<uint64_t>(M), static_cast<uint64_t>(K),
@@ -226,7 +229,7 @@ fgfp8_status launch_gemm(const uint8_t* Xq, const void* Xs, int64_t ld_s, const 
   st = make_map_u8_sw128(&mBh, Wq, static_cast<uint64_t>(b_rows), static_cast<uint64_t>(K), static_cast<uint64_t>(K),
                          BN / 2, dev);
   if (st != FGFP8_OK) return st;
-  auto kernel = fgfp8::gemm_blockscaled_kernel<BN, CW, FMT, kGrouped, kFuse>;
+  auto kernel = fgfp8::gemm_blockscaled_kernel<BN, CW, FMT, kGrouped, kFuse, kEpi>;
   st = set_smem(reinterpret_cast<const void*>(kernel), C::kSmemBytes, dev);
   if (st != FGFP8_OK) return st;
   if (C::kRegSplit) {
@@ -259,14 +262,14 @@ fgfp8_status launch_gemm(const uint8_t* Xq, const void* Xs, int64_t ld_s, const 
                           mB, mBh, Xs, static_cast<uint32_t>(ld_s), Ws, reinterpret_cast<__nv_bfloat16*>(Y),
                           static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), offs, E, cap,
                           static_cast<int>(items), static_cast<int>(num_full), early, Hq, Hs,
-                          static_cast<uint32_t>(ld_h), withhold_kb, dense_group_m(M, K, C::kBM));
+                          static_cast<uint32_t>(ld_h), withhold_kb, dense_group_m(M, K, C::kBM), epi);
 }
 
 // UE8M0 launch with hardware block scaling (persistent, 128 x BN tiles).
-template <int BN, bool kGrouped>
+template <int BN, bool kGrouped, bool kEpi = false>
 fgfp8_status launch_gemm_mx(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq, const void* Ws,
                             void* Y, int64_t M, int64_t N, int64_t K, const int32_t* offs, int E, int64_t b_rows,
-                            cudaStream_t stream, int dev, int sm_count, int early, int cap, int withhold_kb = -1) {
+                            cudaStream_t stream, int dev, int sm_count, int early, int cap, int withhold_kb = -1, const fgfp8::EpiArgs& epi = {}) {
   using C = fgfp8::MxCfg<BN>;
   CUtensorMap mA, mB, mBh;
   fgfp8_status st = make_map_u8_sw128(&mA, Xq, static_cast<uint64_t>(M), static_cast<uint64_t>(K),
@@ -278,7 +281,7 @@ fgfp8_status launch_gemm_mx(const uint8_t* Xq, const void* Xs, int64_t ld_s, con
   st = make_map_u8_sw128(&mBh, Wq, static_cast<uint64_t>(b_rows), static_cast<uint64_t>(K), static_cast<uint64_t>(K),
                          C::kBN / 2, dev);
   if (st != FGFP8_OK) return st;
-  auto kernel = fgfp8::gemm_mx_kernel<BN, kGrouped>;
+  auto kernel = fgfp8::gemm_mx_kernel<BN, kGrouped, kEpi>;
   st = set_smem(reinterpret_cast<const void*>(kernel), C::kSmemBytes, dev);
   if (st != FGFP8_OK) return st;
   const int64_t tiles = ((M + C::kBM - 1) / C::kBM) * (N / C::kBN);
@@ -299,7 +302,7 @@ fgfp8_status launch_gemm_mx(const uint8_t* Xq, const void* Xs, int64_t ld_s, con
                           static_cast<uint32_t>(ld_s), reinterpret_cast<const uint8_t*>(Ws),
                           reinterpret_cast<__nv_bfloat16*>(Y), static_cast<int>(M), static_cast<int>(N),
                           static_cast<int>(K), offs, E, cap, static_cast<int>(items), static_cast<int>(num_full),
-                          early, withhold_kb, dense_group_m(M, K, C::kBM));
+                          early, withhold_kb, dense_group_m(M, K, C::kBM), epi);
 }
 
 template <bool kGrouped>
@@ -670,6 +673,203 @@ fgfp8_status quant_act_masked_impl(const void* X, int64_t ldx, const int32_t* co
   return check_launch("masked quant_act launch");
 }
 
+// Launch with programmatic stream serialization (as launch_dependent) in
+// clusters of S CTAs along x.
+template <typename... KArgs, typename... Args>
+fgfp8_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned threads, size_t smem, int S,
+                            cudaStream_t stream, const char* what, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(S);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = S > 1 ? 2 : 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return ok();
+}
+
+// One few-token kernel.  `blocks`: the most pieces of work that K blocks are
+// not needed to make (128-row weight blocks, or pairs of an expert and a
+// block).  When they leave resident CTAs idle, K is split over clusters of
+// up to kMaxS CTAs; GateUp strides over its pieces with at most one resident
+// wave, the others launch one cluster per piece.
+template <int MODE, int NT, bool kBf16>
+fgfp8_status launch_few(const uint8_t* W, uint64_t rows, fgfp8::FewArgs a, int64_t blocks, cudaStream_t stream,
+                        int dev, int sm_count, const char* what) {
+  using C = fgfp8::FewCfg<MODE, NT>;
+  CUtensorMap mW;
+  const uint64_t K = static_cast<uint64_t>(a.KB) * 128;
+  fgfp8_status st = make_map_u8_sw128(&mW, W, rows, K, K, 128 * C::kTiles, dev);
+  if (st != FGFP8_OK) return st;
+  auto kernel = fgfp8::few_kernel<MODE, NT, kBf16>;
+  st = set_smem(reinterpret_cast<const void*>(kernel), C::kSmemBytes, dev);
+  if (st != FGFP8_OK) return st;
+  const int64_t slots = static_cast<int64_t>(sm_count) * C::kCtas;
+  a.lgS = 0;
+  while ((2 << a.lgS) <= C::kMaxS && (blocks << (a.lgS + 1)) <= slots && (2 << a.lgS) <= a.KB) ++a.lgS;
+  int64_t clusters = blocks;
+  if (MODE == fgfp8::kFewGateUp && clusters > (slots >> a.lgS)) clusters = slots >> a.lgS;
+  return launch_cluster(kernel, static_cast<unsigned>(clusters << a.lgS), C::kThreads, C::kSmemBytes, 1 << a.lgS,
+                        stream, what, mW, a);
+}
+
+// Checks of the epilogue's arguments for an [M, N] output.
+fgfp8_status check_epilogue(const void* bias, int bias_type, int act, const void* residual, int64_t ld_r, int64_t N) {
+  if (act < FGFP8_ACT_NONE || act > FGFP8_ACT_GELU_TANH)
+    return fail(FGFP8_ERR_INVALID_ARG, "act must be one of fgfp8_act (0..4)");
+  if (bias_type != FGFP8_BF16 && bias_type != FGFP8_F32)
+    return fail(FGFP8_ERR_INVALID_ARG, "bias_type must be FGFP8_BF16 (0) or FGFP8_F32 (1)");
+  if (!aligned(bias, 16)) return fail(FGFP8_ERR_ALIGN, "bias must be 16-byte aligned");
+  if (residual) {
+    if (ld_r < N) return fail(FGFP8_ERR_SHAPE, "ld_r must be >= the output's row length");
+    if (!aligned(residual, 16) || ld_r % 8 != 0)
+      return fail(FGFP8_ERR_ALIGN, "residual must be 16-byte aligned with ld_r % 8 == 0");
+  }
+  return FGFP8_OK;
+}
+
+fgfp8::EpiArgs make_epilogue(const void* bias, int bias_type, int act, const void* residual, int64_t ld_r) {
+  fgfp8::EpiArgs e{};
+  e.bias = bias;
+  e.bias_f32 = bias_type == FGFP8_F32;
+  e.act = act;
+  e.residual = reinterpret_cast<const __nv_bfloat16*>(residual);
+  e.ld_r = static_cast<uint64_t>(ld_r);
+  return e;
+}
+
+// The few-token linear kernel (M <= 64): from bf16 rows X (kBf16), or from
+// codes and scales.
+template <bool kBf16>
+fgfp8_status few_linear(const void* src, int64_t ld_src, const void* Xs, int64_t ld_s, const uint8_t* Wq,
+                        const void* Ws, void* Y, int64_t M, int64_t N, int64_t K, int fmt, const fgfp8::EpiArgs& epi,
+                        cudaStream_t stream, int dev, int sm_count, int early) {
+  fgfp8::FewArgs a{};
+  a.src = src;
+  a.ld_src = static_cast<uint64_t>(ld_src);
+  a.src_scale = Xs;
+  a.ld_s = static_cast<uint64_t>(ld_s);
+  a.Ws = Ws;
+  a.fmt = fmt;
+  a.T = static_cast<int>(M);
+  a.KB = static_cast<int>(K / 128);
+  a.NB = static_cast<int>(N / 128);
+  a.Y = reinterpret_cast<__nv_bfloat16*>(Y);
+  a.N = static_cast<int>(N);
+  a.epi = epi;
+  a.early = early;
+  const char* what = "few-token linear launch";
+  if (M <= 16)
+    return launch_few<fgfp8::kFewLinear, 16, kBf16>(Wq, static_cast<uint64_t>(N), a, a.NB, stream, dev, sm_count, what);
+  return launch_few<fgfp8::kFewLinear, 64, kBf16>(Wq, static_cast<uint64_t>(N), a, a.NB, stream, dev, sm_count, what);
+}
+
+// Dense GEMM with its epilogue; with dry set, only validates.
+fgfp8_status gemm_epilogue_impl(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq, const void* Ws,
+                                void* Y, int64_t M, int64_t N, int64_t K, int fmt, const void* bias, int bias_type,
+                                int act, const void* residual, int64_t ld_r, void* stream, int early, bool dry) {
+  if (M == 0 && fmt >= 0 && fmt <= 1 && N >= 0 && K >= 0) return ok();
+  fgfp8_status st = check_gemm_common(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt);
+  if (st != FGFP8_OK) return st;
+  st = check_epilogue(bias, bias_type, act, residual, ld_r, N);
+  if (st != FGFP8_OK) return st;
+  if (dry) return FGFP8_OK;
+  int dev;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != FGFP8_OK) return st;
+  const fgfp8::EpiArgs epi = make_epilogue(bias, bias_type, act, residual, ld_r);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int sms = info.sm_count;
+  if (M <= fgfp8::kFewMaxTokens)
+    return few_linear<false>(Xq, K, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt, epi, s, dev, sms, early);
+  // tiles as in dispatch_gemm
+  if (fmt == FGFP8_SCALE_UE8M0)
+    return N % 256 == 0 ? launch_gemm_mx<256, false, true>(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, nullptr, 1, N, s, dev,
+                                                           sms, early, 0, -1, epi)
+                        : launch_gemm_mx<128, false, true>(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, nullptr, 1, N, s, dev,
+                                                           sms, early, 0, -1, epi);
+  return N % 256 == 0 ? launch_gemm<256, 128, 0, false, false, true>(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, nullptr, 1, N,
+                                                                     s, dev, sms, early, 0, nullptr, nullptr, 0, -1, epi)
+                      : launch_gemm<128, 64, 0, false, false, true>(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, nullptr, 1, N, s,
+                                                                    dev, sms, early, 0, nullptr, nullptr, 0, -1, epi);
+}
+
+// Workspace of fgfp8_moe_decode: the codes of H [T * topk, I], then its scales.
+int64_t moe_codes_bytes(int64_t T, int64_t topk, int64_t I) { return (T * topk * I + 255) / 256 * 256; }
+int64_t moe_workspace_need(int64_t T, int64_t topk, int64_t I) {
+  return moe_codes_bytes(T, topk, I) + T * topk * (I / 128) * 4;
+}
+
+fgfp8_status check_moe_sizes(int64_t T, int64_t topk, int64_t I) {
+  if (T < 0 || topk < 0 || I < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
+  if (T > fgfp8::kFewMaxTokens) return fail(FGFP8_ERR_SHAPE, "T must be <= FGFP8_MOE_MAX_TOKENS (64)");
+  if (topk < 1 || topk > fgfp8::kFewMaxTopk) return fail(FGFP8_ERR_SHAPE, "topk must be in [1, 16]");
+  if (I == 0 || I % 128 != 0) return fail(FGFP8_ERR_SHAPE, "I must be a positive multiple of 128");
+  if (I > (int64_t(1) << 20)) return fail(FGFP8_ERR_SHAPE, "I must be <= 2^20");
+  return FGFP8_OK;
+}
+
+template <int NT>
+fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const float* weights, const uint8_t* W13q,
+                        const void* W13s, const uint8_t* W2q, const void* W2s, const fgfp8::EpiArgs& epi, void* Y,
+                        uint8_t* ws, int64_t T, int64_t topk, int64_t E, int64_t K, int64_t I, int fmt,
+                        cudaStream_t s, int dev, int sms) {
+  fgfp8::FewArgs a{};
+  a.fmt = fmt;
+  a.T = static_cast<int>(T);
+  a.ids = ids;
+  a.wts = weights;
+  a.topk = static_cast<int>(topk);
+  a.E = static_cast<int>(E);
+  a.Hq = ws;
+  a.Hs = reinterpret_cast<float*>(ws + moe_codes_bytes(T, topk, I));
+  a.I = static_cast<int>(I);
+  const int64_t most = E < T * topk ? E : T * topk;            // experts that the tokens can meet
+  // gate/up: [E, 2I, K]
+  a.src = X;
+  a.ld_src = static_cast<uint64_t>(ldx);
+  a.Ws = W13s;
+  a.KB = static_cast<int>(K / 128);
+  a.NB = static_cast<int>(2 * I / 128);
+  fgfp8_status st = launch_few<fgfp8::kFewGateUp, NT, true>(W13q, static_cast<uint64_t>(E) * 2 * I, a, most * (I / 128),
+                                                            s, dev, sms, "expert gate/up launch");
+  if (st != FGFP8_OK) return st;
+  // down: [E, K, I]
+  a.src = a.Hq;
+  a.ld_src = static_cast<uint64_t>(I);
+  a.src_scale = a.Hs;
+  a.Ws = W2s;
+  a.KB = static_cast<int>(I / 128);
+  a.NB = static_cast<int>(K / 128);
+  a.Y = reinterpret_cast<__nv_bfloat16*>(Y);
+  a.N = static_cast<int>(K);
+  a.epi = epi;
+  return launch_few<fgfp8::kFewDown, NT, false>(W2q, static_cast<uint64_t>(E) * K, a, a.NB, s, dev, sms,
+                                                "expert down launch");
+}
+
+template <bool kSigmoid, typename In>
+fgfp8_status launch_route(const fgfp8::RouteArgs& a, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((a.T + fgfp8::kRouteWarps - 1) / fgfp8::kRouteWarps);
+  const unsigned threads = fgfp8::kRouteWarps * 32;
+  if (a.E <= 32) fgfp8::route_topk_kernel<1, kSigmoid, In><<<grid, threads, 0, s>>>(a);
+  else if (a.E <= 64) fgfp8::route_topk_kernel<2, kSigmoid, In><<<grid, threads, 0, s>>>(a);
+  else if (a.E <= 128) fgfp8::route_topk_kernel<4, kSigmoid, In><<<grid, threads, 0, s>>>(a);
+  else if (a.E <= 256) fgfp8::route_topk_kernel<8, kSigmoid, In><<<grid, threads, 0, s>>>(a);
+  else fgfp8::route_topk_kernel<16, kSigmoid, In><<<grid, threads, 0, s>>>(a);
+  return check_launch("route_topk launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -955,6 +1155,147 @@ fgfp8_status fgfp8_gather_cols(const void* parts, int64_t P, int64_t M, int64_t 
   return check_launch("gather_cols launch");
 }
 
+fgfp8_status fgfp8_gemm_epilogue(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq, const void* Ws,
+                                 void* Y, int64_t M, int64_t N, int64_t K, int fmt, const void* bias, int bias_type,
+                                 int act, const void* residual, int64_t ld_r, void* stream) {
+  return gemm_epilogue_impl(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt, bias, bias_type, act, residual, ld_r, stream, 0,
+                            false);
+}
+
+fgfp8_status fgfp8_linear_epilogue(const void* X, int64_t ldx, uint8_t* Xq, void* Xs, int64_t ld_s, const uint8_t* Wq,
+                                   const void* Ws, void* Y, int64_t M, int64_t N, int64_t K, int fmt,
+                                   const void* bias, int bias_type, int act, const void* residual, int64_t ld_r,
+                                   void* stream) {
+  if (M >= 1 && M <= FGFP8_FUSED_QUANT_TOKENS) {
+    // one kernel: X is quantized where the GEMM reads it, Xq and Xs are not used
+    fgfp8_status st = check_fmt(fmt);
+    if (st != FGFP8_OK) return st;
+    if (N < 0 || K < 0 || ldx < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
+    if (K == 0 || K % 128 != 0) return fail(FGFP8_ERR_SHAPE, "K must be a positive multiple of 128");
+    if (N == 0 || N % 128 != 0) return fail(FGFP8_ERR_SHAPE, "N must be a positive multiple of 128");
+    if (N >= (int64_t(1) << 31) || K >= (int64_t(1) << 31)) return fail(FGFP8_ERR_SHAPE, "N and K must be < 2^31");
+    if (ldx < K) return fail(FGFP8_ERR_SHAPE, "ldx must be >= K");
+    if (!X || !Wq || !Ws || !Y) return fail(FGFP8_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (!aligned(X, 16) || ldx % 8 != 0) return fail(FGFP8_ERR_ALIGN, "X must be 16-byte aligned with ldx % 8 == 0");
+    if (!aligned(Wq, 16) || !aligned(Y, 16)) return fail(FGFP8_ERR_ALIGN, "Wq and Y must be 16-byte aligned");
+    if (fmt == FGFP8_SCALE_F32 && !aligned(Ws, 4)) return fail(FGFP8_ERR_ALIGN, "fp32 Ws must be 4-byte aligned");
+    st = check_epilogue(bias, bias_type, act, residual, ld_r, N);
+    if (st != FGFP8_OK) return st;
+    int dev;
+    DeviceInfo info;
+    st = current_device(&dev, &info);
+    if (st != FGFP8_OK) return st;
+    return few_linear<true>(X, ldx, nullptr, 0, Wq, Ws, Y, M, N, K, fmt,
+                            make_epilogue(bias, bias_type, act, residual, ld_r),
+                            reinterpret_cast<cudaStream_t>(stream), dev, info.sm_count, 0);
+  }
+  fgfp8_status st = quant_act_impl(X, M, K, ldx, Xq, Xs, ld_s, fmt, stream, true);
+  if (st != FGFP8_OK) return st;
+  st = gemm_epilogue_impl(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt, bias, bias_type, act, residual, ld_r, stream, 1, true);
+  if (st != FGFP8_OK) return st;
+  st = quant_act_impl(X, M, K, ldx, Xq, Xs, ld_s, fmt, stream, false);
+  if (st != FGFP8_OK) return st;
+  return gemm_epilogue_impl(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt, bias, bias_type, act, residual, ld_r, stream, 1,
+                            false);
+}
+
+fgfp8_status fgfp8_route_topk(const void* logits, int logits_type, int64_t ld, const float* bias, int64_t T, int64_t E,
+                              int64_t topk, int score, int64_t n_group, int64_t topk_group, int renormalize,
+                              float scale, int32_t* ids, float* weights, void* stream) {
+  if (logits_type != FGFP8_BF16 && logits_type != FGFP8_F32)
+    return fail(FGFP8_ERR_INVALID_ARG, "logits_type must be FGFP8_BF16 (0) or FGFP8_F32 (1)");
+  if (score != FGFP8_ROUTE_SOFTMAX && score != FGFP8_ROUTE_SIGMOID)
+    return fail(FGFP8_ERR_INVALID_ARG, "score must be FGFP8_ROUTE_SOFTMAX (0) or FGFP8_ROUTE_SIGMOID (1)");
+  if (renormalize != 0 && renormalize != 1) return fail(FGFP8_ERR_INVALID_ARG, "renormalize must be 0 or 1");
+  if (T < 0 || E < 0 || topk < 0 || ld < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
+  if (T >= (int64_t(1) << 31)) return fail(FGFP8_ERR_SHAPE, "T must be < 2^31");
+  if (E < 1 || E > fgfp8::kFewMaxExperts) return fail(FGFP8_ERR_SHAPE, "E must be in [1, 512]");
+  if (ld < E) return fail(FGFP8_ERR_SHAPE, "ld must be >= E");
+  if (topk < 1 || topk > fgfp8::kFewMaxTopk || topk > E) return fail(FGFP8_ERR_SHAPE, "topk must be in [1, min(E, 16)]");
+  if (n_group < 1 || n_group > 32 || E % n_group != 0)
+    return fail(FGFP8_ERR_SHAPE, "n_group must be in [1, 32] and divide E");
+  if (topk_group < 1 || topk_group > n_group) return fail(FGFP8_ERR_SHAPE, "topk_group must be in [1, n_group]");
+  if (bias && score != FGFP8_ROUTE_SIGMOID)
+    return fail(FGFP8_ERR_UNSUPPORTED, "a selection bias goes with sigmoid scores only");
+  if (T == 0) return ok();
+  if (!logits || !ids || !weights) return fail(FGFP8_ERR_INVALID_ARG, "logits, ids or weights is NULL");
+  if (!aligned(logits, logits_type == FGFP8_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) ||
+      !aligned(weights, 4))
+    return fail(FGFP8_ERR_ALIGN, "logits, bias, ids and weights must be aligned to their elements");
+  int dev;
+  DeviceInfo info;
+  fgfp8_status st = current_device(&dev, &info);
+  if (st != FGFP8_OK) return st;
+  fgfp8::RouteArgs a{};
+  a.logits = logits;
+  a.ld = static_cast<uint64_t>(ld);
+  a.bias = bias;
+  a.T = static_cast<int>(T);
+  a.E = static_cast<int>(E);
+  a.topk = static_cast<int>(topk);
+  a.n_group = static_cast<int>(n_group);
+  a.topk_group = static_cast<int>(topk_group);
+  a.renormalize = renormalize;
+  a.scale = scale;
+  a.ids = ids;
+  a.weights = weights;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (score == FGFP8_ROUTE_SIGMOID)
+    return logits_type == FGFP8_F32 ? launch_route<true, float>(a, s) : launch_route<true, __nv_bfloat16>(a, s);
+  return logits_type == FGFP8_F32 ? launch_route<false, float>(a, s) : launch_route<false, __nv_bfloat16>(a, s);
+}
+
+fgfp8_status fgfp8_moe_workspace_bytes(int64_t T, int64_t topk, int64_t I, int64_t* bytes) {
+  fgfp8_status st = check_moe_sizes(T, topk, I);
+  if (st != FGFP8_OK) return st;
+  if (!bytes) return fail(FGFP8_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = moe_workspace_need(T, topk, I);
+  return ok();
+}
+
+fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, const float* weights,
+                              const uint8_t* W13q, const void* W13s, const uint8_t* W2q, const void* W2s,
+                              const void* residual, int64_t ld_r, void* Y, void* workspace, int64_t workspace_bytes,
+                              int64_t T, int64_t topk, int64_t E, int64_t K, int64_t I, int fmt, void* stream) {
+  fgfp8_status st = check_fmt(fmt);
+  if (st != FGFP8_OK) return st;
+  if (E < 0 || K < 0 || ldx < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
+  st = check_moe_sizes(T, topk, I);
+  if (st != FGFP8_OK) return st;
+  if (E < 1 || E > fgfp8::kFewMaxExperts) return fail(FGFP8_ERR_SHAPE, "E must be in [1, 512]");
+  if (K == 0 || K % 128 != 0) return fail(FGFP8_ERR_SHAPE, "K must be a positive multiple of 128");
+  if (K > (int64_t(1) << 20)) return fail(FGFP8_ERR_SHAPE, "K must be <= 2^20");
+  if (E * 2 * I >= (int64_t(1) << 31) || E * K >= (int64_t(1) << 31))
+    return fail(FGFP8_ERR_SHAPE, "E*2*I and E*K must be < 2^31");
+  if (ldx < K) return fail(FGFP8_ERR_SHAPE, "ldx must be >= K");
+  if (T == 0) return ok();
+  if (!X || !ids || !weights || !W13q || !W13s || !W2q || !W2s || !Y || !workspace)
+    return fail(FGFP8_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(X, 16) || ldx % 8 != 0) return fail(FGFP8_ERR_ALIGN, "X must be 16-byte aligned with ldx % 8 == 0");
+  if (!aligned(W13q, 16) || !aligned(W2q, 16) || !aligned(Y, 16))
+    return fail(FGFP8_ERR_ALIGN, "W13q, W2q and Y must be 16-byte aligned");
+  if (!aligned(ids, 4) || !aligned(weights, 4)) return fail(FGFP8_ERR_ALIGN, "ids and weights must be 4-byte aligned");
+  if (fmt == FGFP8_SCALE_F32 && (!aligned(W13s, 4) || !aligned(W2s, 4)))
+    return fail(FGFP8_ERR_ALIGN, "fp32 W13s and W2s must be 4-byte aligned");
+  if (!aligned(workspace, 256)) return fail(FGFP8_ERR_ALIGN, "workspace must be 256-byte aligned");
+  if (workspace_bytes < moe_workspace_need(T, topk, I))
+    return fail(FGFP8_ERR_SHAPE, "workspace_bytes is below fgfp8_moe_workspace_bytes");
+  st = check_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r, K);
+  if (st != FGFP8_OK) return st;
+  int dev;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != FGFP8_OK) return st;
+  const fgfp8::EpiArgs epi = make_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T <= 16)
+    return launch_moe<16>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
+                          info.sm_count);
+  return launch_moe<64>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
+                        info.sm_count);
+}
+
 fgfp8_status fgfp8_selftest_expired_wait(void* stream) {
   int dev;
   DeviceInfo info;
@@ -1009,6 +1350,8 @@ fgfp8_status fgfp8_check_device_status(void* stream) {
                   "[0, cap]");
     case fgfp8::kDevBadIndex:
       return fail(FGFP8_ERR_DEVICE, "a debug-build index check failed (a tile, row, column or expert out of bounds)");
+    case fgfp8::kDevBadExpert:
+      return fail(FGFP8_ERR_DEVICE, "an expert id is >= E (its slot was skipped)");
     case fgfp8::kDevBadScale:
       return fail(FGFP8_ERR_DEVICE, "the static quantizer's scale is not positive (<= 0 or NaN)");
     default:

@@ -34,6 +34,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "epilogue.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 
@@ -257,16 +258,17 @@ __device__ __forceinline__ void issue_mmas(uint32_t a_base, uint32_t b_base, int
 // of h = SiLU(gate) * up: the up warp of each TMEM lane quadrant hands its
 // bf16 outputs to the gate warp through shared memory, and the gate warp's
 // thread then holds one token's whole 1 x 128 group of h.
-template <int BN, int CW, int FMT, bool kGrouped, bool kFuse = false>
+template <int BN, int CW, int FMT, bool kGrouped, bool kFuse = false, bool kEpi = false>
 __global__ void __launch_bounds__(GemmCfg<BN, CW>::kThreads, 1)
     gemm_blockscaled_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                             const __grid_constant__ CUtensorMap tmBh, const void* __restrict__ Xs, uint32_t ld_s,
                             const void* __restrict__ Ws, __nv_bfloat16* __restrict__ Y, int M, int N, int K,
                             const int32_t* __restrict__ group_offs, int E, int cap, int num_tiles, int num_full,
                             int early_b, uint8_t* __restrict__ Hq, float* __restrict__ Hs, uint32_t ld_h,
-                            int withhold_kb, int group_m) {
+                            int withhold_kb, int group_m, const __grid_constant__ EpiArgs epi) {
   using C = GemmCfg<BN, CW>;
   static_assert(!kFuse || (BN == 256 && CW == 128 && FMT == 0 && !kGrouped), "fused SwiGLU: dense fp32 256-wide");
+  static_assert(!kEpi || (!kGrouped && !kFuse), "bias, activation and residual: dense output only");
   static_assert(C::kStages > C::kNumBuf, "the promotion waits on the stage barriers (see the promotion loop)");
   static_assert((2 * C::kStages + C::kNumBuf + 1 + 8) * 8 + 4 <= C::kBarrierBytes, "barrier area");
   constexpr bool kHalfTiles = !kGrouped && BN == 256 && !kFuse;
@@ -668,18 +670,31 @@ __global__ void __launch_bounds__(GemmCfg<BN, CW>::kThreads, 1)
       uint8_t* slot = sStg + ew * C::kWarpStageBytes;
 #pragma unroll
       for (int p = 0; p < COLS / 64; ++p) {
+        [[maybe_unused]] uint4 res[8];              // kEpi: this row's residual of the pass, all loads in flight
+        if constexpr (kEpi) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            res[c] = live ? load_residual8(epi, m, n0 + col0 + p * 64 + c * 8) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const int j = p * 64 + c * 8;
           uint4 v;
-          __nv_bfloat162 h0 = __floats2bfloat162_rn(acc2[j / 2 + 0].x, acc2[j / 2 + 0].y);
-          __nv_bfloat162 h1 = __floats2bfloat162_rn(acc2[j / 2 + 1].x, acc2[j / 2 + 1].y);
-          __nv_bfloat162 h2 = __floats2bfloat162_rn(acc2[j / 2 + 2].x, acc2[j / 2 + 2].y);
-          __nv_bfloat162 h3 = __floats2bfloat162_rn(acc2[j / 2 + 3].x, acc2[j / 2 + 3].y);
-          v.x = *reinterpret_cast<uint32_t*>(&h0);
-          v.y = *reinterpret_cast<uint32_t*>(&h1);
-          v.z = *reinterpret_cast<uint32_t*>(&h2);
-          v.w = *reinterpret_cast<uint32_t*>(&h3);
+          if constexpr (kEpi) {
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[2 * q] = acc2[j / 2 + q].x, x[2 * q + 1] = acc2[j / 2 + q].y;
+            v = epilogue8(x, epi, n0 + col0 + j, res[c]);
+          } else {
+            __nv_bfloat162 h0 = __floats2bfloat162_rn(acc2[j / 2 + 0].x, acc2[j / 2 + 0].y);
+            __nv_bfloat162 h1 = __floats2bfloat162_rn(acc2[j / 2 + 1].x, acc2[j / 2 + 1].y);
+            __nv_bfloat162 h2 = __floats2bfloat162_rn(acc2[j / 2 + 2].x, acc2[j / 2 + 2].y);
+            __nv_bfloat162 h3 = __floats2bfloat162_rn(acc2[j / 2 + 3].x, acc2[j / 2 + 3].y);
+            v.x = *reinterpret_cast<uint32_t*>(&h0);
+            v.y = *reinterpret_cast<uint32_t*>(&h1);
+            v.z = *reinterpret_cast<uint32_t*>(&h2);
+            v.w = *reinterpret_cast<uint32_t*>(&h3);
+          }
           *reinterpret_cast<uint4*>(slot + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
         }
         __syncwarp();
@@ -775,14 +790,15 @@ struct MxCfg {
                                        kSfSlots * static_cast<size_t>(kSfABytes + kSfBBytes) + kBarrierBytes;
 };
 
-template <int BN, bool kGrouped>
+template <int BN, bool kGrouped, bool kEpi = false>
 __global__ void __launch_bounds__(MxCfg<BN>::kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmBh, const uint8_t* __restrict__ Xs, uint32_t ld_s,
                    const uint8_t* __restrict__ Ws, __nv_bfloat16* __restrict__ Y, int M, int N, int K,
                    const int32_t* __restrict__ group_offs, int E, int cap, int num_tiles, int num_full,
-                   int early_b, int withhold_kb, int group_m) {
+                   int early_b, int withhold_kb, int group_m, const __grid_constant__ EpiArgs epi) {
   using C = MxCfg<BN>;
+  static_assert(!kEpi || !kGrouped, "bias, activation and residual: dense output only");
   constexpr bool kHalfTiles = !kGrouped && BN == 256;
   static_assert(C::kSfCol + C::kSfSlots * C::kSfColsPerSlot <= C::kTmemCols, "TMEM columns");
   static_assert((2 * C::kStages + 4 + 1 + 2 * C::kSfSlots) * 8 + 4 <= C::kBarrierBytes, "barrier area");
@@ -1117,14 +1133,21 @@ __global__ void __launch_bounds__(MxCfg<BN>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 128; j += 8) {
           uint4 v;
-          __nv_bfloat162 h0 = __floats2bfloat162_rn(__uint_as_float(p[j + 0]), __uint_as_float(p[j + 1]));
-          __nv_bfloat162 h1 = __floats2bfloat162_rn(__uint_as_float(p[j + 2]), __uint_as_float(p[j + 3]));
-          __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(p[j + 4]), __uint_as_float(p[j + 5]));
-          __nv_bfloat162 h3 = __floats2bfloat162_rn(__uint_as_float(p[j + 6]), __uint_as_float(p[j + 7]));
-          v.x = *reinterpret_cast<uint32_t*>(&h0);
-          v.y = *reinterpret_cast<uint32_t*>(&h1);
-          v.z = *reinterpret_cast<uint32_t*>(&h2);
-          v.w = *reinterpret_cast<uint32_t*>(&h3);
+          if constexpr (kEpi) {
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = __uint_as_float(p[j + q]);
+            v = epilogue8(x, epi, n0 + col0 + j, load_residual8(epi, m, n0 + col0 + j));
+          } else {
+            __nv_bfloat162 h0 = __floats2bfloat162_rn(__uint_as_float(p[j + 0]), __uint_as_float(p[j + 1]));
+            __nv_bfloat162 h1 = __floats2bfloat162_rn(__uint_as_float(p[j + 2]), __uint_as_float(p[j + 3]));
+            __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(p[j + 4]), __uint_as_float(p[j + 5]));
+            __nv_bfloat162 h3 = __floats2bfloat162_rn(__uint_as_float(p[j + 6]), __uint_as_float(p[j + 7]));
+            v.x = *reinterpret_cast<uint32_t*>(&h0);
+            v.y = *reinterpret_cast<uint32_t*>(&h1);
+            v.z = *reinterpret_cast<uint32_t*>(&h2);
+            v.w = *reinterpret_cast<uint32_t*>(&h3);
+          }
           *reinterpret_cast<uint4*>(yrow + j) = v;
         }
       }

@@ -18,6 +18,7 @@ enum : int {
   kDevTimeoutSelftest = 5,
   kDevBadScale = 6,
   kDevBadIndex = 7,
+  kDevBadExpert = 8,
 };
 
 // The device status word: the first nonzero code a kernel records stays

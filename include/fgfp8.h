@@ -66,6 +66,29 @@ typedef enum {
   FGFP8_ERR_DEVICE = 7       /* a kernel rejected its device-side inputs (device status) */
 } fgfp8_status;
 
+/* Element type of an operand that comes in two types. */
+typedef enum {
+  FGFP8_BF16 = 0,
+  FGFP8_F32 = 1
+} fgfp8_type;
+
+/* Activation of the GEMM epilogue; silu(x) = x / (1 + exp(-x)), gelu(x) =
+ * x/2 (1 + erf(x / sqrt 2)), gelu_tanh(x) = x/2 (1 + tanh(sqrt(2/pi) (x +
+ * 0.044715 x^3))). */
+typedef enum {
+  FGFP8_ACT_NONE = 0,
+  FGFP8_ACT_RELU = 1,
+  FGFP8_ACT_SILU = 2,
+  FGFP8_ACT_GELU = 3,
+  FGFP8_ACT_GELU_TANH = 4
+} fgfp8_act;
+
+/* Scores of the expert router. */
+typedef enum {
+  FGFP8_ROUTE_SOFTMAX = 0,
+  FGFP8_ROUTE_SIGMOID = 1
+} fgfp8_route_score;
+
 /* FGFP8_VERSION of the loaded library. */
 int fgfp8_version(void);
 
@@ -209,6 +232,105 @@ fgfp8_status fgfp8_linear(const void* X, int64_t ldx, uint8_t* Xq, void* Xs, int
 fgfp8_status fgfp8_grouped_linear(const void* X, int64_t ldx, uint8_t* Xq, void* Xs, int64_t ld_s,
                                   const uint8_t* Wq, const void* Ws, void* Y, const int32_t* group_offs,
                                   int32_t E, int64_t M_total, int64_t N, int64_t K, int fmt, void* stream);
+
+/*
+ * The linear layer with its epilogue: Y = bf16( act( X W^T + bias ) +
+ * residual ), every step of the epilogue in fp32 and one rounding to bf16 at
+ * the end.  No counterpart on the pages, whose layers have no bias: it serves
+ * projections with a bias, feed-forward layers with one activation, and
+ * output projections that add to the residual stream.
+ *   bias       [N] bf16 or fp32 (bias_type, an fgfp8_type), 16-byte aligned;
+ *              NULL: none.
+ *   act        an fgfp8_act.
+ *   residual   bf16 [M, N], row stride ld_r elements (ld_r >= N, ld_r % 8 ==
+ *              0, 16-byte aligned); NULL: none (ld_r is then ignored).  It may
+ *              be Y itself (ld_r == N), and must not overlap Y in any other
+ *              way.
+ * The other arguments are those of fgfp8_gemm / fgfp8_linear, except that
+ * fgfp8_linear_epilogue neither reads nor writes Xq and Xs when M <=
+ * FGFP8_FUSED_QUANT_TOKENS: it then quantizes X inside the GEMM, and Xq and
+ * Xs may be NULL.  Within act, NaN stays NaN.
+ */
+#define FGFP8_FUSED_QUANT_TOKENS 16
+
+fgfp8_status fgfp8_gemm_epilogue(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq, const void* Ws,
+                                 void* Y, int64_t M, int64_t N, int64_t K, int fmt, const void* bias, int bias_type,
+                                 int act, const void* residual, int64_t ld_r, void* stream);
+
+fgfp8_status fgfp8_linear_epilogue(const void* X, int64_t ldx, uint8_t* Xq, void* Xs, int64_t ld_s, const uint8_t* Wq,
+                                   const void* Ws, void* Y, int64_t M, int64_t N, int64_t K, int fmt,
+                                   const void* bias, int bias_type, int act, const void* residual, int64_t ld_r,
+                                   void* stream);
+
+/*
+ * The router of an expert layer (no counterpart on the pages, which start
+ * from grouped rows): scores z [T, E] -> each token's topk experts and their
+ * weights, as fgfp8_moe_decode takes them.
+ *   logits   bf16 or fp32 [T, E] (logits_type, an fgfp8_type), row stride ld
+ *            elements (ld >= E).
+ *   score    FGFP8_ROUTE_SOFTMAX: key_e = z_e, p = softmax(z) over all E;
+ *            FGFP8_ROUTE_SIGMOID: key_e = sigmoid(z_e) + bias_e, p_e =
+ *            sigmoid(z_e).  Sigmoid keys are formed and compared in 64 bits.
+ *   bias     float [E], only for the selection and only with sigmoid scores;
+ *            NULL: none.
+ *   n_group, topk_group  the experts form n_group runs of E / n_group; a
+ *            group scores its largest key (softmax) or the sum of its two
+ *            largest (sigmoid; the one that it has, if only one can be
+ *            chosen), and only experts of the topk_group best groups compete.
+ *            1, 1: no groups.
+ *   renormalize  1: the chosen p's are divided by their sum (at least 1e-20).
+ *   scale    factor on every weight.
+ *   ids      int32 [T, topk], weights float [T, topk], in descending order
+ *            of the keys; equal keys and group scores go to the lower index.
+ * An expert whose logit or key is -inf or NaN is never chosen; a token with
+ * fewer than topk experts left gets id -1 and weight 0 in its last slots.
+ * A softmax logit of +inf takes the whole weight, shared by all such logits.
+ * 1 <= E <= 512, 1 <= topk <= min(E, 16), n_group <= 32 and E % n_group == 0.
+ */
+fgfp8_status fgfp8_route_topk(const void* logits, int logits_type, int64_t ld, const float* bias, int64_t T, int64_t E,
+                              int64_t topk, int score, int64_t n_group, int64_t topk_group, int renormalize,
+                              float scale, int32_t* ids, float* weights, void* stream);
+
+/*
+ * A whole SwiGLU expert layer for a few tokens (decode), in two kernels; the
+ * grouped and masked calls above serve larger batches.  For token t:
+ *   (g, u) = W13[e] x_hat          x_hat: fgfp8_quant_act of x_t
+ *   h      = silu(g) * u           in fp32, quantized per 1x128 group straight
+ *                                  from fp32 (amax, scale and code as in
+ *                                  fgfp8_quant_act): h_hat
+ *   Y[t]   = bf16( residual[t] + sum_j weights[t, j] * W2[ids[t, j]] h_hat )
+ * in fp32 with one rounding at the end.
+ *   X        bf16 [T, K], row stride ldx (ldx >= K, ldx % 8 == 0, 16-byte
+ *            aligned).
+ *   ids      int32 [T, topk]: an expert, or a negative value for an empty
+ *            slot (a padded token, an expert that lives elsewhere).  An id >=
+ *            E is skipped, and fgfp8_check_device_status then reports
+ *            FGFP8_ERR_DEVICE.  A token may name an expert twice: the weights
+ *            add up.  A token without an expert gets its residual, or 0.
+ *   weights  float [T, topk].
+ *   W13q, W13s  [E, 2I, K] E4M3 and [E, 2I/128, K/128] scales of gate and up,
+ *            interleaved in 128-row blocks as for fgfp8_gemm_swiglu_quant.
+ *   W2q, W2s [E, K, I] E4M3 and [E, K/128, I/128] scales.
+ *   residual bf16 [T, K], row stride ld_r (ld_r >= K, ld_r % 8 == 0, 16-byte
+ *            aligned), or NULL.  It may be Y itself (ld_r == K).
+ *   Y        bf16 [T, K], 16-byte aligned.  X, ids and weights must not
+ *            overlap Y or the workspace.
+ *   workspace  device memory of at least fgfp8_moe_workspace_bytes, 256-byte
+ *            aligned; it needs no clearing.  Calls that may overlap on the
+ *            GPU need workspaces of their own.
+ * 0 <= T <= FGFP8_MOE_MAX_TOKENS, 1 <= topk <= 16, 1 <= E <= 512, K % 128 ==
+ * 0, I % 128 == 0, K and I <= 2^20, E*2I and E*K < 2^31.  Results do not
+ * depend on the order of ids within other tokens or on timing.
+ */
+#define FGFP8_MOE_MAX_TOKENS 64
+
+/* *bytes (host memory): the workspace of fgfp8_moe_decode at these sizes. */
+fgfp8_status fgfp8_moe_workspace_bytes(int64_t T, int64_t topk, int64_t I, int64_t* bytes);
+
+fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, const float* weights,
+                              const uint8_t* W13q, const void* W13s, const uint8_t* W2q, const void* W2s,
+                              const void* residual, int64_t ld_r, void* Y, void* workspace, int64_t workspace_bytes,
+                              int64_t T, int64_t topk, int64_t E, int64_t K, int64_t I, int fmt, void* stream);
 
 /*
  * Scale granularity per row or per tensor ("FP8 W8A8", "Applying
@@ -382,7 +504,8 @@ fgfp8_status fgfp8_selftest_gemm_timeout(const uint8_t* Xq, const void* Xs, int6
  * the kernels set when they give up.  It returns FGFP8_OK,
  * FGFP8_ERR_TIMEOUT (a barrier wait ran past its one-second limit),
  * FGFP8_ERR_DEVICE (inconsistent group offsets, a masked count outside
- * [0, cap], or a static scale that is not positive) or FGFP8_ERR_CUDA.
+ * [0, cap], an expert id >= E, or a static scale that is not positive) or
+ * FGFP8_ERR_CUDA.
  */
 fgfp8_status fgfp8_check_device_status(void* stream);
 
