@@ -9,18 +9,24 @@
 // (p numbers the pairs of an expert e and a token t routed to it.)  Operands
 // are swapped: 128 weight rows are the MMA's M, the tokens its N (16 to 64
 // columns), so an expert's few tokens waste no weight bandwidth.  Roles of
-// the CTA's 10 warps:
-//   warps 0..3  promotion and epilogue: thread = weight row; per 128-wide K
-//               block the partial of each token from TMEM times sa * sw into
-//               fp32 accumulators;
-//   warps 4..7  token operand: gather the expert's token rows, quantize them
-//               (bf16 source) or copy their codes, write the 128-byte-swizzled
-//               tile and the products sa * sw into the stage.  The rows are
-//               L2-resident, and quantizing them again per weight block costs
-//               a few instructions per 16 KB of weights, which saves a
-//               quantizer kernel and the gather of rows;
-//   warp 8      TMA for the weight tiles;
-//   warp 9      owns TMEM, issues the MMAs.
+// the CTA's warps:
+//   promotion   (4 or 8 warps) thread = weight row; per 128-wide K block the
+//               partial of each token from TMEM times sa * sw into fp32
+//               accumulators, then the epilogue;
+//   tokens      (4 warps) each K block belongs to one of them in turn: from bf16 rows it gathers the
+//               expert's token rows, quantizes them and writes the 128-byte-
+//               swizzled tile; in both cases it writes the products sa * sw.
+//               The rows are L2-resident, and quantizing them again per weight
+//               block costs a few instructions per 16 KB of weights, which
+//               saves a quantizer kernel and the gather of rows.  One warp per
+//               block, so that four blocks' loads overlap: the proxy fence
+//               before a block is handed over waits for all of its thread's
+//               loads (measured with all four warps on every block: 87 us
+//               for M = 37, N = 18432, K = 7168);
+//   TMA         (1 warp) the weight tiles and, where the source is codes, the
+//               token rows (a linear layer's rows are contiguous, and an
+//               expert's rows of H are);
+//   MMA         (1 warp) owns TMEM, issues the MMAs.
 //
 // Few rows leave fewer 128-row weight blocks than SMs, so K is split over the
 // CTAs of a cluster.  Their partial sums meet in distributed shared memory:
@@ -81,7 +87,13 @@ struct FewCfg {
   // holds max(kRedTok, S) tokens
   static constexpr int kRedTok = MODE == kFewGateUp ? 4 : 8;
   static constexpr int kMaxS = kRedTok;
-  static constexpr uint32_t kRedBytes = kRedTok * kTiles * 512;
+  // Promotion warpgroups: group g takes the 16-token chunks g, g + 2, ....
+  // Two for the wide tile: one group's chain of waits, TMEM loads and FMAs
+  // per K block would outlast the 16 KB of weights it covers.
+  static constexpr int kGroups = NT == 64 ? 2 : 1;
+  static constexpr int kEpiWarps = 4 * kGroups;
+  static constexpr int kChunks = NT / 16 / kGroups;                  // chunks per group
+  static constexpr uint32_t kRedBytes = kGroups * kRedTok * kTiles * 512;
   static constexpr uint32_t kAccBytes = MODE == kFewDown ? NT * 512 : 0;
   static constexpr int kPairs = NT * kFewMaxTopk;
   static constexpr int kActive = kPairs < kFewMaxExperts ? kPairs : kFewMaxExperts;
@@ -90,7 +102,7 @@ struct FewCfg {
   static constexpr uint32_t kListBytes = MODE == kFewLinear ? 0 : kActive * 4;      // expert ids and first pairs, u16
   static constexpr uint32_t kWeightBytes = MODE == kFewDown ? kPairs * 6 : 0;       // fp32 weights, i16 ids
   static constexpr uint32_t kAmaxBytes = MODE == kFewGateUp ? 2 * 4 * NT * 4 : 0;
-  static constexpr uint32_t kBarrierBytes = 256;
+  static constexpr uint32_t kBarrierBytes = NT == 64 ? 320 : 256;
   // Two CTAs per SM while the token tile is small: one CTA's ramp and
   // epilogue run under the other's stream.
   static constexpr int kCtas = NT == 16 ? 2 : 1;
@@ -101,13 +113,19 @@ struct FewCfg {
   static constexpr int kStagesFit = static_cast<int>((kBudget - kFixed) / kStageBytes);
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
   static constexpr size_t kSmemBytes = 1024 + kFixed + static_cast<size_t>(kStages) * kStageBytes;
+  // Warps that prepare token operands, K block u by warp u % kTokWarps.  At
+  // most kStages: a warp that has passed its wait for block u - kTokWarps
+  // knows that block u - kTokWarps - kStages is consumed, and its parity
+  // wait for block u tells phases apart only if that covers u - 2 kStages.
+  static constexpr int kTokWarps = kStages < 4 ? kStages : 4;
   static constexpr int kNumBuf = MODE == kFewGateUp && NT == 64 ? 2 : 4;             // TMEM partial buffers
   static constexpr uint32_t kBufCols = kTiles * NT;
   static constexpr uint32_t kTmemCols = kNumBuf * kBufCols;                          // 64, 128 or 256
-  static constexpr int kThreads = 320;
+  static constexpr int kThreads = (kEpiWarps + 6) * 32;
   static_assert(kStages >= 3, "pipeline depth");
+  static_assert(kTokWarps <= kStages && kTokWarps <= 4, "parity waits of the token warps");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols * kCtas <= 512, "TMEM columns");
-  static_assert((2 * kStages + 2 * kNumBuf + 4) * 8 + 16 <= kBarrierBytes, "barrier area");
+  static_assert((2 * kStages + 2 * kNumBuf + 8) * 8 + 16 <= kBarrierBytes, "barrier area");
 };
 
 // ------------------------------------------------------------ cluster helpers
@@ -239,8 +257,9 @@ struct FewIter {
 };
 
 template <int MODE, int NT, bool kBf16>
-__global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
-    few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ FewArgs p) {
+__global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::kCtas)
+    few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+               const __grid_constant__ FewArgs p) {
   using C = FewCfg<MODE, NT>;
   constexpr bool kMoe = MODE != kFewLinear;
   extern __shared__ uint8_t smem_raw[];
@@ -262,33 +281,39 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
   uint64_t* tempty = tfull + C::kNumBuf;
   uint64_t* mma_done = tempty + C::kNumBuf;
   uint64_t* red_full = mma_done + 1;
-  uint64_t* red_empty = red_full + 1;
-  uint64_t* amax_bar = red_empty + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(amax_bar + 1);
+  uint64_t* red_empty = red_full + 2;
+  uint64_t* amax_bar = red_empty + 2;
+  uint64_t* seg_bar = amax_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_bar + 1);
   int* s_active = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kTokWarp0 = C::kEpiWarps, kTmaWarp = kTokWarp0 + 4, kMmaWarp = kTmaWarp + 1;
   const int lgS = p.lgS, S = 1 << lgS;
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster = static_cast<int>(blockIdx.x) >> lgS, clusters = static_cast<int>(gridDim.x) >> lgS;
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1 + 4);                 // the TMA's expect and the four token warps
-      mbar_init(&empty[s], 1 + 4);                // the MMAs and the four promotion warps (scales)
+      mbar_init(&full[s], 1 + 1);                 // the TMA's expect and the block's token warp
+      mbar_init(&empty[s], 1 + C::kEpiWarps);     // the MMAs and the promotion warps (scales)
     }
     for (int b = 0; b < C::kNumBuf; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4);
+      mbar_init(&tempty[b], C::kEpiWarps);
     }
     mbar_init(mma_done, 1);
-    mbar_init(red_full, 4 * S);
-    mbar_init(red_empty, 4 * S);
-    mbar_init(amax_bar, 4);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&red_full[g], 4 * S);
+      mbar_init(&red_empty[g], 4 * S);
+      mbar_init(&amax_bar[g], 4);
+    }
+    mbar_init(seg_bar, C::kEpiWarps);
     fence_mbarrier_init();
     tma_prefetch_desc(&tmW);
+    if (!kBf16) tma_prefetch_desc(&tmX);
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
@@ -350,22 +375,38 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
   const uint32_t tmem_base = *tmem_slot;
   const int active = kMoe ? *s_active : 1;
   FewIter<MODE> work(p, active, sAct, rank, cluster, clusters);
-  FewSeg sg;
+  FewSeg sg{};
   // tokens of a segment's expert
   auto tokens_of = [&](const FewSeg& s) -> uint64_t {
     if constexpr (kMoe) return sMask[s.e];
     return p.T >= 64 ? ~0ull : (1ull << p.T) - 1ull;
   };
   const bool weights_early = MODE == kFewDown || (MODE == kFewLinear && p.early);
-  if (!(warp == 8 && weights_early)) griddep_wait();
+  if (!(warp == kTmaWarp && weights_early)) griddep_wait();
 
-  if (warp == 8) {
+  if (warp == kTmaWarp) {
     if (lane == 0) {
-      // ================= weight tiles
+      // ================= weight tiles, and token tiles of codes
+      const FewIter<MODE> from_start = work;
       uint32_t it = 0;
       bool ok = true;
+      auto weights = [&](uint32_t u, int kb) {
+        const int row = (sg.e * p.NB + (MODE == kFewGateUp ? 2 * sg.j : sg.j)) * 128;
+        const int s = u % C::kStages;
+        const uint32_t b_bytes = kBf16 ? 0u : static_cast<uint32_t>(((__popcll(tokens_of(sg)) + 15) & ~15) * 128);
+        mbar_arrive_expect_tx(&full[s], C::kABytes + b_bytes);
+        tma_load_2d(sA + s * C::kABytes, &tmW, &full[s], kb * 128, row);
+      };
+      // the first stages' weights, before the wait where that is allowed
+      uint32_t pre = 0;
+      if (weights_early) {
+        while (pre < static_cast<uint32_t>(C::kStages) && work.next(sg))
+          for (int kb = sg.kb0; kb < sg.kb1 && pre < static_cast<uint32_t>(C::kStages); ++kb, ++pre) weights(pre, kb);
+        work = from_start;
+        griddep_wait();
+      }
       while (ok && work.next(sg)) {
-        const int row = (MODE == kFewGateUp) ? (sg.e * p.NB + 2 * sg.j) * 128 : (sg.e * p.NB + sg.j) * 128;
+        const int n16 = (__popcll(tokens_of(sg)) + 15) >> 4;
         for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
           const int s = it % C::kStages;
           if (it >= static_cast<uint32_t>(C::kStages) && !mbar_wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u)) {
@@ -373,15 +414,19 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[s], C::kABytes);
-          tma_load_2d(sA + s * C::kABytes, &tmW, &full[s], kb * 128, row);
+          if (it >= pre) weights(it, kb);
+          if constexpr (!kBf16) {
+            const int row = MODE == kFewDown ? sBase[sg.a] : 0;
+            for (int c = 0; c < n16; ++c)
+              tma_load_2d(sB + s * C::kBBytes + c * 2048, &tmX, &full[s], kb * 128, row + c * 16);
+          }
         }
       }
       // every copy issued must land before the CTA may exit
       for (uint32_t i = (it > static_cast<uint32_t>(C::kStages) ? it - C::kStages : 0); i < it; ++i)
         if (!mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1u)) record_status(kDevTimeoutProducer);
     }
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     if (lane == 0) {
       // ================= MMA issuer
       const uint64_t a_desc0 = smem_desc_k_sw128(smem_u32(sA)), b_desc0 = smem_desc_k_sw128(smem_u32(sB));
@@ -414,156 +459,204 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
       mma_commit(mma_done);
       if (!mbar_wait(mma_done, 0)) record_status(kDevTimeoutMma);
     }
-  } else if (warp >= 4) {
-    // ================= token operand: 16 teams of 8 lanes, team q the tokens
-    // q, q + 16, ...; a lane holds 16 of its group's 128 elements
-    constexpr int kPass = NT / 16;
-    constexpr int kAhead = kBf16 ? 2 : 4;                            // K blocks loaded ahead
-    constexpr int kWords = kBf16 ? 2 : 1;                            // 16-byte words per lane and token
-    const int team = (tid - 128) >> 3, l8 = tid & 7;
-    uint32_t it = 0;
-    bool ok = true;
-    uint4 v[kAhead][kPass][kWords];
-    uint32_t sa[kAhead][kPass], sw[kAhead][C::kTiles];
+  } else if (warp >= kTokWarp0) {
+    // ================= token operand and scales of every fourth K block
+    uint32_t it = 0;                                                 // blocks before the segment
+    uint32_t mine = static_cast<uint32_t>(warp - kTokWarp0);         // this warp's next block
+    bool ok = warp - kTokWarp0 < C::kTokWarps;
     while (ok && work.next(sg)) {
+      const uint32_t it_end = it + static_cast<uint32_t>(sg.kb1 - sg.kb0);
       const uint64_t m = tokens_of(sg);
       const int n = __popcll(m);
-      const uint8_t* row[kPass];                                     // this lane's bytes of the token's row
-      uint64_t srow[kPass];                                          // codes: the token's first scale
-#pragma unroll
-      for (int q = 0; q < kPass; ++q) {
-        const int i = q * 16 + team;
-        row[q] = nullptr;
-        srow[q] = 0;
-        if (i < n) {
-          if constexpr (kBf16) {
-            const int t = nth_bit(m, i);
-            row[q] = reinterpret_cast<const uint8_t*>(p.src) + 2 * (static_cast<uint64_t>(t) * p.ld_src) + l8 * 32;
-          } else {
-            const uint64_t r = MODE == kFewDown ? sBase[sg.a] + i : i;
-            row[q] = reinterpret_cast<const uint8_t*>(p.src) + r * p.ld_src + l8 * 16;
-            srow[q] = MODE == kFewDown ? r * p.KB : r;
-          }
-        }
-      }
-      const uint64_t wrow = (MODE == kFewGateUp ? static_cast<uint64_t>(sg.e) * p.NB + 2 * sg.j
-                                                : static_cast<uint64_t>(sg.e) * p.NB + sg.j) * p.KB;
-      auto fetch = [&](int d, int kb) {
-        if (kb >= sg.kb1) return;
+      const uint64_t wrow = (static_cast<uint64_t>(sg.e) * p.NB + (MODE == kFewGateUp ? 2 * sg.j : sg.j)) * p.KB;
+      uint32_t sw[C::kTiles];
+      auto load_sw = [&](int kb) {
 #pragma unroll
         for (int t = 0; t < C::kTiles; ++t)
-          sw[d][t] = load_scale_word(p.Ws, wrow + static_cast<uint64_t>(t) * p.KB + kb, p.fmt);
+          sw[t] = load_scale_word(p.Ws, wrow + static_cast<uint64_t>(t) * p.KB + kb, p.fmt);
+      };
+      // this unit's stage is free
+      auto stage_free = [&](uint32_t u) {
+        const bool free = u < static_cast<uint32_t>(C::kStages) ||
+                          mbar_wait(&empty[u % C::kStages], ((u / C::kStages) & 1u) ^ 1u);
+        if (__all_sync(0xFFFFFFFFu, free)) return true;
+        if (lane == 0) record_status(kDevTimeoutProducer);
+        return false;
+      };
+
+      if constexpr (kBf16) {
+        // lane: team lane / 8 of a group of four tokens, 16 elements of the
+        // 128; 16 tokens (four groups) are in registers at a time
+        const int team = lane >> 3, l8 = lane & 7;
+        constexpr int kTok = (NT + 31) / 32;
+        int tok[kTok];
 #pragma unroll
-        for (int q = 0; q < kPass; ++q) {
-          sa[d][q] = 0;
+        for (int q = 0; q < kTok; ++q) tok[q] = q * 32 + lane < n ? (kMoe ? nth_bit(m, q * 32 + lane) : q * 32 + lane) : 0;
+        uint4 v[4][2];
+        auto load16 = [&](int c, int kb) {
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) v[d][q][w] = make_uint4(0, 0, 0, 0);
-          if (q * 16 + team < n) {
-            const uint4* g = reinterpret_cast<const uint4*>(row[q] + static_cast<uint64_t>(kb) * (128 * kWords));
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) v[d][q][w] = MODE == kFewDown ? g[w] : __ldg(g + w);
-            if constexpr (!kBf16) {
-              if (MODE == kFewDown)                                  // written by GateUp: a plain load
-                sa[d][q] = reinterpret_cast<const uint32_t*>(p.src_scale)[srow[q] + kb];
-              else
-                sa[d][q] = load_scale_word(p.src_scale, srow[q] + static_cast<uint64_t>(kb) * p.ld_s, p.fmt);
+          for (int q = 0; q < 4; ++q) {
+            if (c * 16 + q * 4 >= n) break;
+            const int i = c * 16 + q * 4 + team;
+            const int t = __shfl_sync(0xFFFFFFFFu, tok[kTok == 1 ? 0 : c >> 1], i & 31);
+            v[q][0] = v[q][1] = make_uint4(0, 0, 0, 0);
+            if (i < n) {
+              const uint4* g = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.src) +
+                                                              static_cast<uint64_t>(t) * p.ld_src + kb * 128 + l8 * 16);
+              v[q][0] = __ldg(g);
+              v[q][1] = __ldg(g + 1);
             }
           }
-        }
-      };
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) fetch(d, sg.kb0 + d);
-      for (int kb0 = sg.kb0; kb0 < sg.kb1 && ok; kb0 += kAhead) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-          const int kb = kb0 + d;
-          if (kb >= sg.kb1) break;
-          const int s = it % C::kStages;
-          if (it >= static_cast<uint32_t>(C::kStages) &&
-              !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u))) {
-            if (lane == 0) record_status(kDevTimeoutProducer);
-            ok = false;
-            break;
-          }
+        };
+        auto store16 = [&](int c, int s) {
           uint8_t* tile = sB + s * C::kBBytes;
           float* sc = sSc + s * C::kTiles * NT;
 #pragma unroll
-          for (int q = 0; q < kPass; ++q) {
-            if (q * 16 >= n) break;
-            const int i = q * 16 + team;
+          for (int q = 0; q < 4; ++q) {
+            if (c * 16 + q * 4 >= n) break;
+            const int i = c * 16 + q * 4 + team;
+            const uint4 x = v[q][0], y = v[q][1];
+            uint32_t am = max(absmax_bits8(x), absmax_bits8(y));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
             uint4 codes;
             float scale;
-            if constexpr (kBf16) {
-              const uint4 x = v[d][q][0], y = v[d][q][1];
-              uint32_t am = max(absmax_bits8(x), absmax_bits8(y));
-#pragma unroll
-              for (int o = 1; o < 8; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-              auto quant = [&](auto tag) {
-                constexpr int F = decltype(tag)::value;
-                const GroupScale g = make_scale<F>(am);
-                codes.x = quant4<F>(x.x, x.y, g);
-                codes.y = quant4<F>(x.z, x.w, g);
-                codes.z = quant4<F>(y.x, y.y, g);
-                codes.w = quant4<F>(y.z, y.w, g);
-                scale = F == 0 ? g.s : scale_value(g.e8, 1);
-              };
-              if (p.fmt == 0) quant(std::integral_constant<int, 0>{});
-              else quant(std::integral_constant<int, 1>{});
-            } else {
-              codes = v[d][q][0];
-              scale = MODE == kFewDown ? __uint_as_float(sa[d][q]) : scale_value(sa[d][q], p.fmt);
-            }
+            auto quant = [&](auto tag) {
+              constexpr int F = decltype(tag)::value;
+              const GroupScale g = make_scale<F>(am);
+              codes.x = quant4<F>(x.x, x.y, g);
+              codes.y = quant4<F>(x.z, x.w, g);
+              codes.z = quant4<F>(y.x, y.y, g);
+              codes.w = quant4<F>(y.z, y.w, g);
+              scale = F == 0 ? g.s : scale_value(g.e8, 1);
+            };
+            if (p.fmt == 0) quant(std::integral_constant<int, 0>{});
+            else quant(std::integral_constant<int, 1>{});
             if (i < n) {
               // chunk l8 of row i at l8 ^ (i % 8): the 128-byte swizzle of a TMA tile
               *reinterpret_cast<uint4*>(tile + i * 128 + ((l8 ^ (i & 7)) << 4)) = codes;
               if (l8 == 0) {
 #pragma unroll
-                for (int t = 0; t < C::kTiles; ++t) sc[t * NT + i] = scale * scale_value(sw[d][t], p.fmt);
+                for (int t = 0; t < C::kTiles; ++t) sc[t * NT + i] = scale * scale_value(sw[t], p.fmt);
               }
             }
           }
-          fetch(d, kb + kAhead);
+        };
+        auto kb_of = [&](uint32_t u) { return sg.kb0 + static_cast<int>(u - it); };
+        if (mine < it_end) {
+          load16(0, kb_of(mine));
+          load_sw(kb_of(mine));
+        }
+        for (; mine < it_end; mine += C::kTokWarps) {
+          const int kb = kb_of(mine);
+          const int s = mine % C::kStages;
+          if (!stage_free(mine)) {
+            ok = false;
+            break;
+          }
+          store16(0, s);
+#pragma unroll
+          for (int c = 1; c < NT / 16; ++c) {
+            if (c * 16 >= n) break;
+            load16(c, kb);
+            store16(c, s);
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&full[s]);
-          ++it;
+          if (mine + C::kTokWarps < it_end) {
+            load16(0, kb + C::kTokWarps);
+            load_sw(kb + C::kTokWarps);
+          }
+        }
+      } else {
+        // lane: the scales of tokens lane, lane + 32
+        constexpr int kTok = (NT + 31) / 32;
+        uint32_t sa[kTok];
+        const uint64_t pair0 = MODE == kFewDown ? sBase[sg.a] : 0;
+        auto load_sa = [&](int kb) {
+#pragma unroll
+          for (int q = 0; q < kTok; ++q) {
+            const int i = q * 32 + lane;
+            sa[q] = 0;
+            if (i < n) {
+              if (MODE == kFewDown)                                  // written by GateUp: a plain load
+                sa[q] = reinterpret_cast<const uint32_t*>(p.src_scale)[(pair0 + i) * p.KB + kb];
+              else
+                sa[q] = load_scale_word(p.src_scale, i + static_cast<uint64_t>(kb) * p.ld_s, p.fmt);
+            }
+          }
+        };
+        auto kb_of = [&](uint32_t u) { return sg.kb0 + static_cast<int>(u - it); };
+        if (mine < it_end) {
+          load_sa(kb_of(mine));
+          load_sw(kb_of(mine));
+        }
+        for (; mine < it_end; mine += C::kTokWarps) {
+          const int kb = kb_of(mine);
+          const int s = mine % C::kStages;
+          if (!stage_free(mine)) {
+            ok = false;
+            break;
+          }
+          float* sc = sSc + s * C::kTiles * NT;
+          const float w = scale_value(sw[0], p.fmt);
+#pragma unroll
+          for (int q = 0; q < kTok; ++q) {
+            const int i = q * 32 + lane;
+            if (i < n) sc[i] = w * (MODE == kFewDown ? __uint_as_float(sa[q]) : scale_value(sa[q], p.fmt));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[s]);
+          if (mine + C::kTokWarps < it_end) {
+            load_sa(kb + C::kTokWarps);
+            load_sw(kb + C::kTokWarps);
+          }
         }
       }
+      it = it_end;
     }
   } else {
     // ================= promotion and epilogue: thread = weight row
-    const int row = tid;                                             // 0..127
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-    uint32_t it = 0, meets = 0, quants = 0;
+    const int grp = C::kGroups == 1 ? 0 : warp >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;                                // 0..127
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    float* red = sRed + grp * (C::kRedBytes / C::kGroups / 4);
+    uint32_t it = 0, meets = 0, segs = 0;
     bool ok = true;
+    auto expired = [&] {
+      if (lane == 0) record_status(kDevTimeoutEpilogue);
+      ok = false;
+    };
+    // first token of this group's chunk q
+    auto chunk0 = [&](int q) { return (q * C::kGroups + grp) * 16; };
 
-    // The ranks' partial sums of 16 tokens t0 + i < n (v[tile][i]): on
+    // The ranks' partial sums of 16 tokens t0 + i < n (val[tile][i]): on
     // return the rank that owns a token (token % S) holds the sum over the
     // ranks, added in rank order; the others' entries are left as they were.
     auto meet = [&](float (&val)[C::kTiles][16], int t0, int n) {
-      const uint32_t red = smem_u32(sRed);
 #pragma unroll
       for (int c = 0; c < 16 / C::kRedTok; ++c) {
         if (t0 + c * C::kRedTok >= n || !ok) break;
-        if (meets > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_empty, (meets - 1) & 1u))) {
-          ok = false;
+        if (meets > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_empty[grp], (meets - 1) & 1u))) {
+          expired();
           break;
         }
-        // token c * kRedTok + q goes to rank q % S (kRedTok % S == 0), slot q / S
+        // token c * kRedTok + q goes to rank q % S (S divides kRedTok), slot q / S
         const int slots = C::kRedTok >> lgS;
 #pragma unroll
         for (int q = 0; q < C::kRedTok; ++q) {
           if (t0 + c * C::kRedTok + q < n) {
             const uint32_t at = static_cast<uint32_t>(((rank * slots + (q >> lgS)) * C::kTiles * 128 + row) * 4);
-            const uint32_t to = map_to_rank(red + at, q & (S - 1));
+            const uint32_t to = map_to_rank(smem_u32(red) + at, q & (S - 1));
 #pragma unroll
             for (int t = 0; t < C::kTiles; ++t) st_cluster_f32(to + t * 512, val[t][c * C::kRedTok + q]);
           }
         }
         __syncwarp();
-        if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(red_full), lane));
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(red_full, meets & 1u))) {
-          ok = false;
+        if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_full[grp]), lane));
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_full[grp], meets & 1u))) {
+          expired();
           break;
         }
 #pragma unroll
@@ -572,56 +665,66 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
 #pragma unroll
             for (int t = 0; t < C::kTiles; ++t) {
               float sum = 0.0f;
-              for (int r = 0; r < S; ++r) sum += sRed[((r * slots + (q >> lgS)) * C::kTiles + t) * 128 + row];
+              for (int r = 0; r < S; ++r) sum += red[((r * slots + (q >> lgS)) * C::kTiles + t) * 128 + row];
               val[t][c * C::kRedTok + q] = sum;
             }
           }
         }
         __syncwarp();
-        if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(red_empty), lane));
+        if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_empty[grp]), lane));
         ++meets;
       }
-      if (!ok && lane == 0) record_status(kDevTimeoutEpilogue);
     };
 
-    float acc[NT / 16][C::kTiles][16];
+    float acc[C::kChunks][C::kTiles][16];
     while (ok && work.next(sg)) {
       const uint64_t m = tokens_of(sg);
       const int n = __popcll(m);
 #pragma unroll
-      for (int c = 0; c < NT / 16; ++c)
+      for (int q = 0; q < C::kChunks; ++q)
 #pragma unroll
         for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c][t][i] = 0.0f;
+          for (int i = 0; i < 16; ++i) acc[q][t][i] = 0.0f;
       for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
         const int b = it % C::kNumBuf, s = it % C::kStages;
-        // The scales were written before the MMAs' operands were complete, but
-        // by other threads: the stage's full barrier orders them.
+        // the scales come from other threads: the stage's full barrier orders them
         if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / C::kStages) & 1u) &&
                                          mbar_wait(&tfull[b], (it / C::kNumBuf) & 1u))) {
-          if (lane == 0) record_status(kDevTimeoutEpilogue);
-          ok = false;
+          expired();
           break;
         }
         tc_fence_after();
         const float4* sc = reinterpret_cast<const float4*>(sSc + s * C::kTiles * NT);
+        // one wait for as many TMEM loads as registers allow
+        constexpr int kBatch = C::kTiles == 1 ? C::kChunks : 1;
 #pragma unroll
-        for (int c = 0; c < NT / 16; ++c) {
-          if (c * 16 >= n) break;
+        for (int q0 = 0; q0 < C::kChunks; q0 += kBatch) {
+          if (chunk0(q0) >= n) break;
+          uint32_t d[kBatch][C::kTiles][16];
 #pragma unroll
-          for (int t = 0; t < C::kTiles; ++t) {
-            uint32_t d[16];
-            tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(b * C::kBufCols + t * NT + c * 16), d);
-            tmem_wait_ld();
+          for (int q = 0; q < kBatch; ++q) {
+            if (chunk0(q0 + q) >= n) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = sc[(t * NT + c * 16) / 4 + i];
-              acc[c][t][4 * i + 0] = __fmaf_rn(__uint_as_float(d[4 * i + 0]), f.x, acc[c][t][4 * i + 0]);
-              acc[c][t][4 * i + 1] = __fmaf_rn(__uint_as_float(d[4 * i + 1]), f.y, acc[c][t][4 * i + 1]);
-              acc[c][t][4 * i + 2] = __fmaf_rn(__uint_as_float(d[4 * i + 2]), f.z, acc[c][t][4 * i + 2]);
-              acc[c][t][4 * i + 3] = __fmaf_rn(__uint_as_float(d[4 * i + 3]), f.w, acc[c][t][4 * i + 3]);
-            }
+            for (int t = 0; t < C::kTiles; ++t)
+              tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(b * C::kBufCols + t * NT + chunk0(q0 + q)), d[q][t]);
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            if (chunk0(q0 + q) >= n) break;
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 f = sc[(t * NT + chunk0(q0 + q)) / 4 + i];
+                float* a = &acc[q0 + q][t][4 * i];
+                const uint32_t* x = &d[q][t][4 * i];
+                a[0] = __fmaf_rn(__uint_as_float(x[0]), f.x, a[0]);
+                a[1] = __fmaf_rn(__uint_as_float(x[1]), f.y, a[1]);
+                a[2] = __fmaf_rn(__uint_as_float(x[2]), f.z, a[2]);
+                a[3] = __fmaf_rn(__uint_as_float(x[3]), f.w, a[3]);
+              }
           }
         }
         tc_fence_before();
@@ -633,44 +736,47 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
       }
       if (!ok) break;
 
+      if constexpr (MODE != kFewDown) {
+        if (S > 1) {
+#pragma unroll
+          for (int q = 0; q < C::kChunks; ++q)
+            if (chunk0(q) < n && ok) meet(acc[q], chunk0(q), n);
+          if (!ok) break;
+        }
+      }
       if constexpr (MODE == kFewGateUp) {
         // h = silu(g) u in fp32, its 1x128 group (the 128 threads' rows)
         // quantized straight from fp32: no rounding to bf16 on the way
+        float* am = sAmax + (segs & 1u) * 4 * NT;
 #pragma unroll
-        for (int c = 0; c < NT / 16; ++c)
-          if (S > 1 && c * 16 < n && ok) meet(acc[c], c * 16, n);
-        if (!ok) break;
-        float* am = sAmax + (quants & 1u) * 4 * NT;
-#pragma unroll
-        for (int c = 0; c < NT / 16; ++c) {
-          if (c * 16 >= n) break;
+        for (int q = 0; q < C::kChunks; ++q) {
+          if (chunk0(q) >= n) break;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (c * 16 + i < n && ((c * 16 + i) & (S - 1)) == rank) {
-              const float g = acc[c][0][i];
-              const float h = __fdiv_rn(g, 1.0f + expf(-g)) * acc[c][1][i];
-              acc[c][0][i] = h;
+            const int ti = chunk0(q) + i;
+            if (ti < n && (i & (S - 1)) == rank) {
+              const float g = acc[q][0][i];
+              const float h = __fdiv_rn(g, 1.0f + expf(-g)) * acc[q][1][i];
+              acc[q][0][i] = h;
               const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
-              if (lane == 0) am[warp * NT + c * 16 + i] = __uint_as_float(top);
+              if (lane == 0) am[quad * NT + ti] = __uint_as_float(top);
             }
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(amax_bar);
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(amax_bar, quants & 1u))) {
-          if (lane == 0) record_status(kDevTimeoutEpilogue);
-          ok = false;
+        if (lane == 0) mbar_arrive(&amax_bar[grp]);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&amax_bar[grp], segs & 1u))) {
+          expired();
           break;
         }
-        ++quants;
         const uint64_t pair0 = sBase[sg.a];
 #pragma unroll
-        for (int c = 0; c < NT / 16; ++c) {
-          if (c * 16 >= n) break;
+        for (int q = 0; q < C::kChunks; ++q) {
+          if (chunk0(q) >= n) break;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int ti = c * 16 + i;
-            if (ti < n && (ti & (S - 1)) == rank) {
+            const int ti = chunk0(q) + i;
+            if (ti < n && (i & (S - 1)) == rank) {
               // magnitude bits compare like the values, and a NaN above all of them
               const uint32_t a01 = max(__float_as_uint(am[ti]), __float_as_uint(am[NT + ti]));
               const uint32_t a23 = max(__float_as_uint(am[2 * NT + ti]), __float_as_uint(am[3 * NT + ti]));
@@ -678,54 +784,52 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
               const uint64_t r = pair0 + ti;
               FGFP8_DCHECK(r < static_cast<uint64_t>(p.T) * p.topk && sg.j * 128 + row < p.I);
               p.Hq[r * p.I + sg.j * 128 + row] =
-                  __nv_cvt_float_to_fp8(__fdiv_rn(acc[c][0][i], scale), __NV_SATFINITE, __NV_E4M3);
+                  __nv_cvt_float_to_fp8(__fdiv_rn(acc[q][0][i], scale), __NV_SATFINITE, __NV_E4M3);
               if (row == 0) p.Hs[r * (p.I / 128) + sg.j] = scale;
             }
           }
         }
       } else if constexpr (MODE == kFewDown) {
         // the expert's tokens, weighted, into the block's fp32 sums; a token
-        // that names the expert in several slots adds their weights
-        constexpr int kW = (NT + 31) / 32;
-        int tok[kW];
-        float wt[kW];
-#pragma unroll
-        for (int q = 0; q < kW; ++q) {
-          const int i = q * 32 + lane;
-          tok[q] = 0;
-          wt[q] = 0.0f;
-          if (i < n) {
-            tok[q] = nth_bit(m, i);
-            for (int k = 0; k < p.topk; ++k)
-              if (sIds[tok[q] * p.topk + k] == sg.e) wt[q] += sWt[tok[q] * p.topk + k];
-          }
+        // that names the expert in several slots adds their weights.  The
+        // groups hold different tokens of one expert, but a token may change
+        // groups from one expert to the next: each expert waits for the last.
+        if (C::kGroups > 1 && segs > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(seg_bar, (segs - 1) & 1u))) {
+          expired();
+          break;
         }
 #pragma unroll
-        for (int c = 0; c < NT / 16; ++c) {
-          if (c * 16 >= n) break;
+        for (int q = 0; q < C::kChunks; ++q) {
+          if (chunk0(q) >= n) break;
+          int tok = 0;
+          float wt = 0.0f;
+          if (lane < 16 && chunk0(q) + lane < n) {
+            tok = nth_bit(m, chunk0(q) + lane);
+            for (int k = 0; k < p.topk; ++k)
+              if (sIds[tok * p.topk + k] == sg.e) wt += sWt[tok * p.topk + k];
+          }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int ti = c * 16 + i;
-            const int t = __shfl_sync(0xFFFFFFFFu, tok[ti / 32], ti % 32);
-            const float w = __shfl_sync(0xFFFFFFFFu, wt[ti / 32], ti % 32);
-            if (ti < n) sAcc[t * 128 + row] = __fmaf_rn(w, acc[c][0][i], sAcc[t * 128 + row]);
+            const int t = __shfl_sync(0xFFFFFFFFu, tok, i);
+            const float w = __shfl_sync(0xFFFFFFFFu, wt, i);
+            if (chunk0(q) + i < n) sAcc[t * 128 + row] = __fmaf_rn(w, acc[q][0][i], sAcc[t * 128 + row]);
           }
         }
+        if (C::kGroups > 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(seg_bar);
+        }
       } else {
-#pragma unroll
-        for (int c = 0; c < NT / 16; ++c)
-          if (S > 1 && c * 16 < n && ok) meet(acc[c], c * 16, n);
-        if (!ok) break;
         const int col = sg.j * 128 + row;
         const float bias = load_bias(p.epi, col);
 #pragma unroll
-        for (int c = 0; c < NT / 16; ++c) {
-          if (c * 16 >= n) break;
+        for (int q = 0; q < C::kChunks; ++q) {
+          if (chunk0(q) >= n) break;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int t = c * 16 + i;
-            if (t < n && (t & (S - 1)) == rank) {
-              float y = apply_act(acc[c][0][i] + bias, p.epi.act);
+            const int t = chunk0(q) + i;
+            if (t < n && (i & (S - 1)) == rank) {
+              float y = apply_act(acc[q][0][i] + bias, p.epi.act);
               if (p.epi.residual) y += __bfloat162float(p.epi.residual[static_cast<uint64_t>(t) * p.epi.ld_r + col]);
               FGFP8_DCHECK(t < p.T && col < p.N);
               p.Y[static_cast<uint64_t>(t) * p.N + col] = __float2bfloat16_rn(y);
@@ -733,23 +837,25 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
           }
         }
       }
+      ++segs;
     }
 
     if constexpr (MODE == kFewDown) {
       // the block's sums over all experts, residual added, one rounding
+      if (C::kGroups > 1 && ok && segs > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(seg_bar, (segs - 1) & 1u))) expired();
       const int col = cluster * 128 + row;
 #pragma unroll
-      for (int c = 0; c < NT / 16; ++c) {
-        if (c * 16 >= p.T || !ok) break;
+      for (int q = 0; q < C::kChunks; ++q) {
+        if (chunk0(q) >= p.T || !ok) break;
         float val[1][16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) val[0][i] = sAcc[(c * 16 + i) * 128 + row];
-        if (S > 1) meet(val, c * 16, p.T);
+        for (int i = 0; i < 16; ++i) val[0][i] = sAcc[(chunk0(q) + i) * 128 + row];
+        if (S > 1) meet(val, chunk0(q), p.T);
         if (!ok) break;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int t = c * 16 + i;
-          if (t < p.T && (t & (S - 1)) == rank) {
+          const int t = chunk0(q) + i;
+          if (t < p.T && (i & (S - 1)) == rank) {
             float y = val[0][i];
             if (p.epi.residual) y += __bfloat162float(p.epi.residual[static_cast<uint64_t>(t) * p.epi.ld_r + col]);
             FGFP8_DCHECK(col < p.N);
@@ -766,7 +872,7 @@ __global__ void __launch_bounds__(320, FewCfg<MODE, NT>::kCtas)
   __syncthreads();
   tc_fence_after();
   if (S > 1) cluster_sync();                      // no rank leaves while another may still write to it
-  if (warp == 9) tmem_dealloc(tmem_base, C::kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem_base, C::kTmemCols);
 }
 
 }  // namespace fgfp8

@@ -703,13 +703,17 @@ fgfp8_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned th
 // up to kMaxS CTAs; GateUp strides over its pieces with at most one resident
 // wave, the others launch one cluster per piece.
 template <int MODE, int NT, bool kBf16>
-fgfp8_status launch_few(const uint8_t* W, uint64_t rows, fgfp8::FewArgs a, int64_t blocks, cudaStream_t stream,
-                        int dev, int sm_count, const char* what) {
+fgfp8_status launch_few(const uint8_t* W, uint64_t rows, uint64_t src_rows, fgfp8::FewArgs a, int64_t blocks,
+                        cudaStream_t stream, int dev, int sm_count, const char* what) {
   using C = fgfp8::FewCfg<MODE, NT>;
-  CUtensorMap mW;
+  CUtensorMap mW, mX{};
   const uint64_t K = static_cast<uint64_t>(a.KB) * 128;
   fgfp8_status st = make_map_u8_sw128(&mW, W, rows, K, K, 128 * C::kTiles, dev);
   if (st != FGFP8_OK) return st;
+  if (!kBf16) {
+    st = make_map_u8_sw128(&mX, a.src, src_rows, K, K, 16, dev);      // token codes, 16 rows per copy
+    if (st != FGFP8_OK) return st;
+  }
   auto kernel = fgfp8::few_kernel<MODE, NT, kBf16>;
   st = set_smem(reinterpret_cast<const void*>(kernel), C::kSmemBytes, dev);
   if (st != FGFP8_OK) return st;
@@ -719,7 +723,7 @@ fgfp8_status launch_few(const uint8_t* W, uint64_t rows, fgfp8::FewArgs a, int64
   int64_t clusters = blocks;
   if (MODE == fgfp8::kFewGateUp && clusters > (slots >> a.lgS)) clusters = slots >> a.lgS;
   return launch_cluster(kernel, static_cast<unsigned>(clusters << a.lgS), C::kThreads, C::kSmemBytes, 1 << a.lgS,
-                        stream, what, mW, a);
+                        stream, what, mW, mX, a);
 }
 
 // Checks of the epilogue's arguments for an [M, N] output.
@@ -769,8 +773,10 @@ fgfp8_status few_linear(const void* src, int64_t ld_src, const void* Xs, int64_t
   a.early = early;
   const char* what = "few-token linear launch";
   if (M <= 16)
-    return launch_few<fgfp8::kFewLinear, 16, kBf16>(Wq, static_cast<uint64_t>(N), a, a.NB, stream, dev, sm_count, what);
-  return launch_few<fgfp8::kFewLinear, 64, kBf16>(Wq, static_cast<uint64_t>(N), a, a.NB, stream, dev, sm_count, what);
+    return launch_few<fgfp8::kFewLinear, 16, kBf16>(Wq, static_cast<uint64_t>(N), static_cast<uint64_t>(M), a, a.NB, stream,
+                                                      dev, sm_count, what);
+  return launch_few<fgfp8::kFewLinear, 64, kBf16>(Wq, static_cast<uint64_t>(N), static_cast<uint64_t>(M), a, a.NB, stream,
+                                                      dev, sm_count, what);
 }
 
 // Dense GEMM with its epilogue; with dry set, only validates.
@@ -841,7 +847,7 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
   a.Ws = W13s;
   a.KB = static_cast<int>(K / 128);
   a.NB = static_cast<int>(2 * I / 128);
-  fgfp8_status st = launch_few<fgfp8::kFewGateUp, NT, true>(W13q, static_cast<uint64_t>(E) * 2 * I, a, most * (I / 128),
+  fgfp8_status st = launch_few<fgfp8::kFewGateUp, NT, true>(W13q, static_cast<uint64_t>(E) * 2 * I, 0, a, most * (I / 128),
                                                             s, dev, sms, "expert gate/up launch");
   if (st != FGFP8_OK) return st;
   // down: [E, K, I]
@@ -854,7 +860,8 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
   a.Y = reinterpret_cast<__nv_bfloat16*>(Y);
   a.N = static_cast<int>(K);
   a.epi = epi;
-  return launch_few<fgfp8::kFewDown, NT, false>(W2q, static_cast<uint64_t>(E) * K, a, a.NB, s, dev, sms,
+  return launch_few<fgfp8::kFewDown, NT, false>(W2q, static_cast<uint64_t>(E) * K, static_cast<uint64_t>(T) * topk, a,
+                                                a.NB, s, dev, sms,
                                                 "expert down launch");
 }
 

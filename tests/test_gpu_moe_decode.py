@@ -131,7 +131,7 @@ def check(Y, ref, tol, what=""):
 @pytest.mark.parametrize("T,E,topk,K,I", [(1, 4, 1, 128, 128), (1, 16, 8, 1024, 256), (2, 3, 3, 256, 384),
                                           (5, 8, 2, 640, 128), (16, 8, 4, 512, 256), (17, 8, 2, 384, 128),
                                           (31, 40, 8, 256, 128), (64, 4, 2, 512, 384), (64, 16, 16, 256, 128),
-                                          (33, 512, 3, 128, 128)])
+                                          (33, 512, 3, 128, 128), (1, 12, 8, 7168, 1024), (20, 3, 2, 4096, 1024)])
 def test_against_the_formula(dev, T, E, topk, K, I, fmt):
     W = weights_for(dev, E, K, I, fmt, seed=T + E)
     X = workloads.activations((T, K), "normal", seed=T)
