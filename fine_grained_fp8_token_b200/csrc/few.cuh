@@ -98,17 +98,20 @@ struct FewCfg {
   static constexpr int kPairs = NT * kFewMaxTopk;
   static constexpr int kActive = kPairs < kFewMaxExperts ? kPairs : kFewMaxExperts;
   using Mask = typename std::conditional<NT == 64, unsigned long long, unsigned int>::type;   // a bit per token
-  static constexpr uint32_t kMaskBytes = MODE == kFewLinear ? 0 : kFewMaxExperts * sizeof(Mask);
-  static constexpr uint32_t kListBytes = MODE == kFewLinear ? 0 : kActive * 4;      // expert ids and first pairs, u16
-  static constexpr uint32_t kWeightBytes = MODE == kFewDown ? kPairs * 6 : 0;       // fp32 weights, i16 ids
-  static constexpr uint32_t kAmaxBytes = MODE == kFewGateUp ? 2 * 4 * NT * 4 : 0;
+  static constexpr bool kMoe = MODE != kFewLinear;
+  static constexpr uint32_t kMaskBytes = kMoe ? kFewMaxExperts * sizeof(Mask) : 0;
+  static constexpr uint32_t kBaseBytes = kMoe ? kFewMaxExperts * 2 : 0;             // first pair of each expert, u16
+  static constexpr uint32_t kActBytes = kMoe ? kActive * 2 : 0;                     // active experts, u16
+  static constexpr uint32_t kTokBytes = kMoe ? kPairs : 0;                          // token of each pair, u8
+  static constexpr uint32_t kWeightBytes = MODE == kFewDown ? kPairs * 4 : 0;       // weight of each pair
+  static constexpr uint32_t kAmaxBytes = MODE == kFewGateUp ? kGroups * 2 * 4 * kRedTok * 4 : 0;
   static constexpr uint32_t kBarrierBytes = NT == 64 ? 320 : 256;
   // Two CTAs per SM while the token tile is small: one CTA's ramp and
   // epilogue run under the other's stream.
   static constexpr int kCtas = NT == 16 ? 2 : 1;
   static constexpr uint32_t kBudget = (kCtas == 2 ? 115712u : 232448u) - 1024u;     // after the 1 KB alignment
   static constexpr uint32_t kFixed =
-      kRedBytes + kAccBytes + kMaskBytes + kListBytes + kWeightBytes + kAmaxBytes + kBarrierBytes;
+      kRedBytes + kAccBytes + kMaskBytes + kBaseBytes + kActBytes + kTokBytes + kWeightBytes + kAmaxBytes + kBarrierBytes;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kScBytes;
   static constexpr int kStagesFit = static_cast<int>((kBudget - kFixed) / kStageBytes);
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
@@ -193,12 +196,6 @@ __device__ __forceinline__ float scale_of_f32(float amax, int fmt) {
   return scale_value(e, 1);
 }
 
-// Position of the i-th set bit of m (i < popcount).
-__device__ __forceinline__ int nth_bit(uint64_t m, int i) {
-  for (; i > 0; --i) m &= m - 1;
-  return __ffsll(static_cast<long long>(m)) - 1;
-}
-
 // ------------------------------------------------------------ work of a CTA
 // A segment: K blocks [kb0, kb1) of one expert's weight rows.
 struct FewSeg {
@@ -256,26 +253,40 @@ struct FewIter {
   }
 };
 
+// A mask of one bit per token: those below t.
+template <typename M>
+__device__ __forceinline__ M bits_below(int t) {
+  return (M(1) << t) - M(1);
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 template <int MODE, int NT, bool kBf16>
 __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::kCtas)
     few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                const __grid_constant__ FewArgs p) {
   using C = FewCfg<MODE, NT>;
-  constexpr bool kMoe = MODE != kFewLinear;
+  using Mask = typename C::Mask;
+  constexpr bool kMoe = C::kMoe;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::kStages * C::kABytes;
   float* sSc = reinterpret_cast<float*>(sB + C::kStages * C::kBBytes);             // [stage][tile][NT]
   float* sAcc = sSc + C::kStages * C::kTiles * NT;                                 // Down: [token][128]
-  float* sRed = sAcc + C::kAccBytes / 4;                                           // [rank][slot][tile][128]
-  typename C::Mask* sMask = reinterpret_cast<typename C::Mask*>(sRed + C::kRedBytes / 4);   // tokens of each expert
-  float* sWt = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sMask) + C::kMaskBytes);   // Down: [T * topk]
-  float* sAmax = sWt + (MODE == kFewDown ? C::kPairs : 0);                         // GateUp: [2][4][NT]
-  uint16_t* sAct = reinterpret_cast<uint16_t*>(sAmax + C::kAmaxBytes / 4);         // active experts
-  uint16_t* sBase = sAct + (kMoe ? C::kActive : 0);                                // their first pairs
-  int16_t* sIds = reinterpret_cast<int16_t*>(sBase + (kMoe ? C::kActive : 0));     // Down: [T * topk]
-  uint64_t* full = reinterpret_cast<uint64_t*>(sIds + (MODE == kFewDown ? C::kPairs : 0));
+  float* sRed = sAcc + C::kAccBytes / 4;                                           // [group][rank][slot][tile][128]
+  Mask* sMask = reinterpret_cast<Mask*>(sRed + C::kRedBytes / 4);                  // tokens of each expert
+  float* sWt = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sMask) + C::kMaskBytes);
+  float* sAmax = sWt + C::kWeightBytes / 4;                                        // GateUp: [group][2][4][kRedTok]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sAmax + C::kAmaxBytes / 4);
   uint64_t* empty = full + C::kStages;
   uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + C::kNumBuf;
@@ -285,7 +296,10 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   uint64_t* amax_bar = red_empty + 2;
   uint64_t* seg_bar = amax_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_bar + 1);
-  int* s_active = reinterpret_cast<int*>(tmem_slot + 1);
+  uint16_t* sBase = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(full) + C::kBarrierBytes);
+  uint16_t* sAct = sBase + C::kBaseBytes / 2;
+  uint8_t* sTok = reinterpret_cast<uint8_t*>(sAct + C::kActBytes / 2);
+  __shared__ int s_count[2][kFewMaxExperts / 32];                                  // per 32 experts: active, pairs
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kTokWarp0 = C::kEpiWarps, kTmaWarp = kTokWarp0 + 4, kMmaWarp = kTmaWarp + 1;
@@ -295,7 +309,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1 + 1);                 // the TMA's expect and the block's token warp
+      mbar_init(&full[s], 1 + 1);                 // the TMA warp and the block's token warp
       mbar_init(&empty[s], 1 + C::kEpiWarps);     // the MMAs and the promotion warps (scales)
     }
     for (int b = 0; b < C::kNumBuf; ++b) {
@@ -327,7 +341,11 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     griddep_wait();
     griddep_launch_dependents();
   }
+  int active = 1;
   if constexpr (kMoe) {
+    // sMask[e]: the tokens routed to e; sAct: the experts with any, ascending;
+    // pair sBase[e] + i: e's i-th token, its weight the sum over the token's
+    // slots that name e
     const int P = p.T * p.topk;
     for (int e = tid; e < p.E; e += C::kThreads) sMask[e] = 0;
     if constexpr (MODE == kFewDown)
@@ -335,37 +353,54 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     __syncthreads();
     for (int i = tid; i < P; i += C::kThreads) {
       const int id = __ldg(p.ids + i);
-      const bool in = id >= 0 && id < p.E;
-      if (in) atomicOr(sMask + id, typename C::Mask(1) << (i / p.topk));
+      if (id >= 0 && id < p.E) atomicOr(sMask + id, Mask(1) << (i / p.topk));
       if (id >= p.E && blockIdx.x == 0) record_status(kDevBadExpert);
-      if constexpr (MODE == kFewDown) {
-        sIds[i] = static_cast<int16_t>(in ? id : -1);
-        sWt[i] = __ldg(p.wts + i);
+    }
+    __syncthreads();
+    const int chunks = (p.E + 31) >> 5;
+    auto mask_of = [&](int e) { return e < p.E ? sMask[e] : Mask(0); };
+    for (int c = warp; c < chunks; c += C::kThreads / 32) {
+      const int k = __popcll(mask_of(c * 32 + lane));
+      const uint32_t on = __ballot_sync(0xFFFFFFFFu, k != 0);
+      const int pairs = __reduce_add_sync(0xFFFFFFFFu, k);
+      if (lane == 0) s_count[0][c] = __popc(on), s_count[1][c] = pairs;
+    }
+    __syncthreads();
+    for (int c = warp; c < chunks; c += C::kThreads / 32) {
+      const int k = __popcll(mask_of(c * 32 + lane));
+      const uint32_t on = __ballot_sync(0xFFFFFFFFu, k != 0);
+      int incl = k;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      // chunks before this one (at most 16)
+      const int na = __reduce_add_sync(0xFFFFFFFFu, lane < c ? s_count[0][lane & 15] : 0);
+      const int np = __reduce_add_sync(0xFFFFFFFFu, lane < c ? s_count[1][lane & 15] : 0);
+      if (k != 0) {
+        sAct[na + __popc(on & ((1u << lane) - 1u))] = static_cast<uint16_t>(c * 32 + lane);
+        sBase[c * 32 + lane] = static_cast<uint16_t>(np + incl - k);
       }
     }
     __syncthreads();
-    if (warp == 0) {
-      int na = 0, np = 0;
-      for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        const uint64_t m = e < p.E ? sMask[e] : 0;
-        const int c = __popcll(m);
-        int incl = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-          if (lane >= d) incl += o;
-        }
-        const uint32_t on = __ballot_sync(0xFFFFFFFFu, c != 0);
-        if (c != 0) {
-          const int a = na + __popc(on & ((1u << lane) - 1u));
-          sAct[a] = static_cast<uint16_t>(e);
-          sBase[a] = static_cast<uint16_t>(np + incl - c);
-        }
-        na += __popc(on);
-        np += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    active = __reduce_add_sync(0xFFFFFFFFu, lane < chunks ? s_count[0][lane & 15] : 0);
+    for (int i = tid; i < P; i += C::kThreads) {
+      const int id = __ldg(p.ids + i);
+      if (id < 0 || id >= p.E) continue;
+      const int t = i / p.topk, j = i - t * p.topk;
+      bool first = true;
+      for (int k = 0; k < j; ++k) first = first && __ldg(p.ids + t * p.topk + k) != id;
+      if (!first) continue;
+      const int at = sBase[id] + __popcll(sMask[id] & bits_below<Mask>(t));
+      FGFP8_DCHECK(at < C::kPairs);
+      sTok[at] = static_cast<uint8_t>(t);
+      if constexpr (MODE == kFewDown) {
+        float w = __ldg(p.wts + i);
+        for (int k = j + 1; k < p.topk; ++k)
+          if (__ldg(p.ids + t * p.topk + k) == id) w += __ldg(p.wts + t * p.topk + k);
+        sWt[at] = w;
       }
-      if (lane == 0) *s_active = na;
     }
   }
   tc_fence_before();
@@ -373,40 +408,26 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   tc_fence_after();
   if (S > 1) cluster_sync();                      // the ranks' barriers exist before anyone arrives on them
   const uint32_t tmem_base = *tmem_slot;
-  const int active = kMoe ? *s_active : 1;
   FewIter<MODE> work(p, active, sAct, rank, cluster, clusters);
   FewSeg sg{};
-  // tokens of a segment's expert
-  auto tokens_of = [&](const FewSeg& s) -> uint64_t {
-    if constexpr (kMoe) return sMask[s.e];
-    return p.T >= 64 ? ~0ull : (1ull << p.T) - 1ull;
+  auto count_of = [&](const FewSeg& s) -> int {   // tokens of a segment
+    if constexpr (kMoe) return __popcll(sMask[s.e]);
+    return p.T;
+  };
+  auto pair0_of = [&](const FewSeg& s) -> int {   // their first pair, or row
+    if constexpr (kMoe) return sBase[s.e];
+    return 0;
   };
   const bool weights_early = MODE == kFewDown || (MODE == kFewLinear && p.early);
   if (!(warp == kTmaWarp && weights_early)) griddep_wait();
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
-      // ================= weight tiles, and token tiles of codes
-      const FewIter<MODE> from_start = work;
+      // ================= weight tiles
       uint32_t it = 0;
       bool ok = true;
-      auto weights = [&](uint32_t u, int kb) {
-        const int row = (sg.e * p.NB + (MODE == kFewGateUp ? 2 * sg.j : sg.j)) * 128;
-        const int s = u % C::kStages;
-        const uint32_t b_bytes = kBf16 ? 0u : static_cast<uint32_t>(((__popcll(tokens_of(sg)) + 15) & ~15) * 128);
-        mbar_arrive_expect_tx(&full[s], C::kABytes + b_bytes);
-        tma_load_2d(sA + s * C::kABytes, &tmW, &full[s], kb * 128, row);
-      };
-      // the first stages' weights, before the wait where that is allowed
-      uint32_t pre = 0;
-      if (weights_early) {
-        while (pre < static_cast<uint32_t>(C::kStages) && work.next(sg))
-          for (int kb = sg.kb0; kb < sg.kb1 && pre < static_cast<uint32_t>(C::kStages); ++kb, ++pre) weights(pre, kb);
-        work = from_start;
-        griddep_wait();
-      }
       while (ok && work.next(sg)) {
-        const int n16 = (__popcll(tokens_of(sg)) + 15) >> 4;
+        const int row = (sg.e * p.NB + (MODE == kFewGateUp ? 2 * sg.j : sg.j)) * 128;
         for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
           const int s = it % C::kStages;
           if (it >= static_cast<uint32_t>(C::kStages) && !mbar_wait(&empty[s], ((it / C::kStages) & 1u) ^ 1u)) {
@@ -414,12 +435,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             ok = false;
             break;
           }
-          if (it >= pre) weights(it, kb);
-          if constexpr (!kBf16) {
-            const int row = MODE == kFewDown ? sBase[sg.a] : 0;
-            for (int c = 0; c < n16; ++c)
-              tma_load_2d(sB + s * C::kBBytes + c * 2048, &tmX, &full[s], kb * 128, row + c * 16);
-          }
+          mbar_arrive_expect_tx(&full[s], C::kABytes);
+          tma_load_2d(sA + s * C::kABytes, &tmW, &full[s], kb * 128, row);
         }
       }
       // every copy issued must land before the CTA may exit
@@ -427,23 +444,25 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
         if (!mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1u)) record_status(kDevTimeoutProducer);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      // ================= MMA issuer
-      const uint64_t a_desc0 = smem_desc_k_sw128(smem_u32(sA)), b_desc0 = smem_desc_k_sw128(smem_u32(sB));
-      uint32_t it = 0;
-      bool ok = true;
-      while (ok && work.next(sg)) {
-        const int n = (__popcll(tokens_of(sg)) + 15) & ~15;
-        const uint32_t idesc = idesc_e4m3_f32(128, n);
-        for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-          const int s = it % C::kStages, b = it % C::kNumBuf;
-          if (!mbar_wait(&full[s], (it / C::kStages) & 1u) ||
-              (it >= static_cast<uint32_t>(C::kNumBuf) && !mbar_wait(&tempty[b], ((it / C::kNumBuf) & 1u) ^ 1u))) {
-            record_status(kDevTimeoutMma);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+    // ================= MMA issuer: the whole warp keeps the loop's state
+    // uniform, one elected lane issues
+    const uint64_t a_desc0 = smem_desc_k_sw128(smem_u32(sA)), b_desc0 = smem_desc_k_sw128(smem_u32(sB));
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && work.next(sg)) {
+      const int n = __shfl_sync(0xFFFFFFFFu, (count_of(sg) + 15) & ~15, 0);
+      const uint32_t idesc = idesc_e4m3_f32(128, n);
+      for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+        const int s = it % C::kStages, b = it % C::kNumBuf;
+        bool got = mbar_wait(&full[s], (it / C::kStages) & 1u);
+        if (it >= static_cast<uint32_t>(C::kNumBuf)) got = got && mbar_wait(&tempty[b], ((it / C::kNumBuf) & 1u) ^ 1u);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          if (lane == 0) record_status(kDevTimeoutMma);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int t = 0; t < C::kTiles; ++t) {
             const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::kBufCols + t * NT);
@@ -455,27 +474,29 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           mma_commit(&empty[s]);
           mma_commit(&tfull[b]);
         }
+        __syncwarp();
       }
-      mma_commit(mma_done);
-      if (!mbar_wait(mma_done, 0)) record_status(kDevTimeoutMma);
     }
+    if (elect_one()) mma_commit(mma_done);
+    __syncwarp();
+    if (!mbar_wait(mma_done, 0) && lane == 0) record_status(kDevTimeoutMma);
   } else if (warp >= kTokWarp0) {
-    // ================= token operand and scales of every fourth K block
+    // ================= token operand and scales of this warp's K blocks
     uint32_t it = 0;                                                 // blocks before the segment
     uint32_t mine = static_cast<uint32_t>(warp - kTokWarp0);         // this warp's next block
     bool ok = warp - kTokWarp0 < C::kTokWarps;
     while (ok && work.next(sg)) {
       const uint32_t it_end = it + static_cast<uint32_t>(sg.kb1 - sg.kb0);
-      const uint64_t m = tokens_of(sg);
-      const int n = __popcll(m);
+      const int n = count_of(sg), pair0 = pair0_of(sg);
       const uint64_t wrow = (static_cast<uint64_t>(sg.e) * p.NB + (MODE == kFewGateUp ? 2 * sg.j : sg.j)) * p.KB;
+      auto kb_of = [&](uint32_t u) { return sg.kb0 + static_cast<int>(u - it); };
       uint32_t sw[C::kTiles];
       auto load_sw = [&](int kb) {
 #pragma unroll
         for (int t = 0; t < C::kTiles; ++t)
           sw[t] = load_scale_word(p.Ws, wrow + static_cast<uint64_t>(t) * p.KB + kb, p.fmt);
       };
-      // this unit's stage is free
+      // block u's stage is free
       auto stage_free = [&](uint32_t u) {
         const bool free = u < static_cast<uint32_t>(C::kStages) ||
                           mbar_wait(&empty[u % C::kStages], ((u / C::kStages) & 1u) ^ 1u);
@@ -485,22 +506,20 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       };
 
       if constexpr (kBf16) {
-        // lane: team lane / 8 of a group of four tokens, 16 elements of the
-        // 128; 16 tokens (four groups) are in registers at a time
+        // lane: team lane / 8 of four, one token per team and pass, 16 of the
+        // token's 128 elements.  Chunks of 16 tokens: four passes together,
+        // so that their loads and reductions overlap, or one for up to four
+        // tokens.
         const int team = lane >> 3, l8 = lane & 7;
-        constexpr int kTok = (NT + 31) / 32;
-        int tok[kTok];
-#pragma unroll
-        for (int q = 0; q < kTok; ++q) tok[q] = q * 32 + lane < n ? (kMoe ? nth_bit(m, q * 32 + lane) : q * 32 + lane) : 0;
         uint4 v[4][2];
-        auto load16 = [&](int c, int kb) {
+        auto load = [&](auto passes, int c, int kb) {
+          constexpr int P = decltype(passes)::value;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (c * 16 + q * 4 >= n) break;
+          for (int q = 0; q < P; ++q) {
             const int i = c * 16 + q * 4 + team;
-            const int t = __shfl_sync(0xFFFFFFFFu, tok[kTok == 1 ? 0 : c >> 1], i & 31);
             v[q][0] = v[q][1] = make_uint4(0, 0, 0, 0);
             if (i < n) {
+              const int t = kMoe ? sTok[pair0 + i] : i;
               const uint4* g = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.src) +
                                                               static_cast<uint64_t>(t) * p.ld_src + kb * 128 + l8 * 16);
               v[q][0] = __ldg(g);
@@ -508,41 +527,54 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             }
           }
         };
-        auto store16 = [&](int c, int s) {
+        auto store = [&](auto passes, auto fmt, int c, int s) {
+          constexpr int P = decltype(passes)::value, F = decltype(fmt)::value;
           uint8_t* tile = sB + s * C::kBBytes;
           float* sc = sSc + s * C::kTiles * NT;
+          uint32_t am[P];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (c * 16 + q * 4 >= n) break;
+          for (int q = 0; q < P; ++q) am[q] = max(absmax_bits8(v[q][0]), absmax_bits8(v[q][1]));
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+            for (int q = 0; q < P; ++q) am[q] = max(am[q], __shfl_xor_sync(0xFFFFFFFFu, am[q], o));
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
             const int i = c * 16 + q * 4 + team;
-            const uint4 x = v[q][0], y = v[q][1];
-            uint32_t am = max(absmax_bits8(x), absmax_bits8(y));
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+            const GroupScale g = make_scale<F>(am[q]);
             uint4 codes;
-            float scale;
-            auto quant = [&](auto tag) {
-              constexpr int F = decltype(tag)::value;
-              const GroupScale g = make_scale<F>(am);
-              codes.x = quant4<F>(x.x, x.y, g);
-              codes.y = quant4<F>(x.z, x.w, g);
-              codes.z = quant4<F>(y.x, y.y, g);
-              codes.w = quant4<F>(y.z, y.w, g);
-              scale = F == 0 ? g.s : scale_value(g.e8, 1);
-            };
-            if (p.fmt == 0) quant(std::integral_constant<int, 0>{});
-            else quant(std::integral_constant<int, 1>{});
+            codes.x = quant4<F>(v[q][0].x, v[q][0].y, g);
+            codes.y = quant4<F>(v[q][0].z, v[q][0].w, g);
+            codes.z = quant4<F>(v[q][1].x, v[q][1].y, g);
+            codes.w = quant4<F>(v[q][1].z, v[q][1].w, g);
+            const float scale = F == 0 ? g.s : scale_value(g.e8, 1);
             if (i < n) {
               // chunk l8 of row i at l8 ^ (i % 8): the 128-byte swizzle of a TMA tile
               *reinterpret_cast<uint4*>(tile + i * 128 + ((l8 ^ (i & 7)) << 4)) = codes;
               if (l8 == 0) {
 #pragma unroll
-                for (int t = 0; t < C::kTiles; ++t) sc[t * NT + i] = scale * scale_value(sw[t], p.fmt);
+                for (int t = 0; t < C::kTiles; ++t) sc[t * NT + i] = scale * scale_value(sw[t], F);
               }
             }
           }
         };
-        auto kb_of = [&](uint32_t u) { return sg.kb0 + static_cast<int>(u - it); };
+        using One = std::integral_constant<int, 1>;
+        using Four = std::integral_constant<int, 4>;
+        auto load16 = [&](int c, int kb) {
+          if (n - c * 16 > 4) load(Four{}, c, kb);
+          else load(One{}, c, kb);
+        };
+        auto store16 = [&](int c, int s) {
+          using F32 = std::integral_constant<int, 0>;
+          using E8 = std::integral_constant<int, 1>;
+          if (n - c * 16 > 4) {
+            if (p.fmt == 0) store(Four{}, F32{}, c, s);
+            else store(Four{}, E8{}, c, s);
+          } else {
+            if (p.fmt == 0) store(One{}, F32{}, c, s);
+            else store(One{}, E8{}, c, s);
+          }
+        };
         if (mine < it_end) {
           load16(0, kb_of(mine));
           load_sw(kb_of(mine));
@@ -555,9 +587,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             break;
           }
           store16(0, s);
-#pragma unroll
-          for (int c = 1; c < NT / 16; ++c) {
-            if (c * 16 >= n) break;
+#pragma unroll 1
+          for (int c = 1; c * 16 < n; ++c) {
             load16(c, kb);
             store16(c, s);
           }
@@ -570,10 +601,10 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           }
         }
       } else {
-        // lane: the scales of tokens lane, lane + 32
+        // lane: the scales of tokens lane, lane + 32; lane 0 requests the rows
         constexpr int kTok = (NT + 31) / 32;
+        const int n16 = (n + 15) >> 4;
         uint32_t sa[kTok];
-        const uint64_t pair0 = MODE == kFewDown ? sBase[sg.a] : 0;
         auto load_sa = [&](int kb) {
 #pragma unroll
           for (int q = 0; q < kTok; ++q) {
@@ -581,13 +612,12 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             sa[q] = 0;
             if (i < n) {
               if (MODE == kFewDown)                                  // written by GateUp: a plain load
-                sa[q] = reinterpret_cast<const uint32_t*>(p.src_scale)[(pair0 + i) * p.KB + kb];
+                sa[q] = reinterpret_cast<const uint32_t*>(p.src_scale)[static_cast<uint64_t>(pair0 + i) * p.KB + kb];
               else
                 sa[q] = load_scale_word(p.src_scale, i + static_cast<uint64_t>(kb) * p.ld_s, p.fmt);
             }
           }
         };
-        auto kb_of = [&](uint32_t u) { return sg.kb0 + static_cast<int>(u - it); };
         if (mine < it_end) {
           load_sa(kb_of(mine));
           load_sw(kb_of(mine));
@@ -607,7 +637,11 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             if (i < n) sc[i] = w * (MODE == kFewDown ? __uint_as_float(sa[q]) : scale_value(sa[q], p.fmt));
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n16 * 2048));
+            for (int c = 0; c < n16; ++c)
+              tma_load_2d(sB + s * C::kBBytes + c * 2048, &tmX, &full[s], kb * 128, pair0 + c * 16);
+          }
           if (mine + C::kTokWarps < it_end) {
             load_sa(kb + C::kTokWarps);
             load_sw(kb + C::kTokWarps);
@@ -622,64 +656,96 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     const int row = quad * 32 + lane;                                // 0..127
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
     float* red = sRed + grp * (C::kRedBytes / C::kGroups / 4);
-    uint32_t it = 0, meets = 0, segs = 0;
+    constexpr int kSubs = C::kChunks * 16 / C::kRedTok;              // meetings of a full tile
+    const int slots = C::kRedTok >> lgS;                             // tokens of a meeting per rank
+    uint32_t it = 0, meets = 0, segs = 0, quants = 0;
     bool ok = true;
     auto expired = [&] {
       if (lane == 0) record_status(kDevTimeoutEpilogue);
       ok = false;
     };
-    // first token of this group's chunk q
+    // first token of this group's chunk q, and of its meeting c
     auto chunk0 = [&](int q) { return (q * C::kGroups + grp) * 16; };
+    auto sub0 = [&](int c) { return chunk0(c * C::kRedTok / 16) + c * C::kRedTok % 16; };
 
-    // The ranks' partial sums of 16 tokens t0 + i < n (val[tile][i]): on
-    // return the rank that owns a token (token % S) holds the sum over the
-    // ranks, added in rank order; the others' entries are left as they were.
-    auto meet = [&](float (&val)[C::kTiles][16], int t0, int n) {
+    // One meeting of the ranks: each thread hands kRedTok tokens' partial sums
+    // of its row (val(q, t)) to the tokens' owners, token q to rank q % S
+    // (S divides kRedTok), slot q / S.  Between meet_put and meet_done the
+    // owner reads sum_of(slot, t), added in rank order.  Alone (S = 1) a
+    // thread meets only itself.
+    auto meet_put = [&](int count, auto val) {
+      if (S > 1 && meets > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_empty[grp], (meets - 1) & 1u))) {
+        expired();
+        return;
+      }
 #pragma unroll
-      for (int c = 0; c < 16 / C::kRedTok; ++c) {
-        if (t0 + c * C::kRedTok >= n || !ok) break;
-        if (meets > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_empty[grp], (meets - 1) & 1u))) {
-          expired();
-          break;
-        }
-        // token c * kRedTok + q goes to rank q % S (S divides kRedTok), slot q / S
-        const int slots = C::kRedTok >> lgS;
+      for (int q = 0; q < C::kRedTok; ++q) {
+        if (q < count) {
+          const int at = ((rank * slots + (q >> lgS)) * C::kTiles) * 128 + row;
+          if (S > 1) {
+            const uint32_t to = map_to_rank(smem_u32(red + at), q & (S - 1));
 #pragma unroll
-        for (int q = 0; q < C::kRedTok; ++q) {
-          if (t0 + c * C::kRedTok + q < n) {
-            const uint32_t at = static_cast<uint32_t>(((rank * slots + (q >> lgS)) * C::kTiles * 128 + row) * 4);
-            const uint32_t to = map_to_rank(smem_u32(red) + at, q & (S - 1));
+            for (int t = 0; t < C::kTiles; ++t) st_cluster_f32(to + t * 512, val(q, t));
+          } else {
 #pragma unroll
-            for (int t = 0; t < C::kTiles; ++t) st_cluster_f32(to + t * 512, val[t][c * C::kRedTok + q]);
+            for (int t = 0; t < C::kTiles; ++t) red[at + t * 128] = val(q, t);
           }
         }
+      }
+      if (S > 1) {
         __syncwarp();
         if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_full[grp]), lane));
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_full[grp], meets & 1u))) {
-          expired();
-          break;
-        }
-#pragma unroll
-        for (int q = 0; q < C::kRedTok; ++q) {
-          if ((q & (S - 1)) == rank && t0 + c * C::kRedTok + q < n) {
-#pragma unroll
-            for (int t = 0; t < C::kTiles; ++t) {
-              float sum = 0.0f;
-              for (int r = 0; r < S; ++r) sum += red[((r * slots + (q >> lgS)) * C::kTiles + t) * 128 + row];
-              val[t][c * C::kRedTok + q] = sum;
-            }
-          }
-        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_full[grp], meets & 1u))) expired();
+      }
+    };
+    auto sum_of = [&](int slot, int t) {
+      float sum = 0.0f;
+      for (int r = 0; r < S; ++r) sum += red[((r * slots + slot) * C::kTiles + t) * 128 + row];
+      return sum;
+    };
+    auto meet_done = [&] {
+      if (S > 1) {
         __syncwarp();
         if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_empty[grp]), lane));
         ++meets;
       }
     };
 
+    // Output rows (Linear, Down): this rank's tokens of meeting c.  Their
+    // residuals are loaded ahead: the first meeting's before the K loop.
+    const int col = (MODE == kFewGateUp ? 0 : cluster) * 128 + row;
+    float bias = 0.0f;
+    uint16_t res[C::kRedTok];
+    auto load_res = [&](int c) {
+#pragma unroll
+      for (int k = 0; k < C::kRedTok; ++k) {
+        const int q = rank + (k << lgS), t = sub0(c) + q;
+        res[k] = 0;
+        if (p.epi.residual != nullptr && q < C::kRedTok && t < p.T)
+          res[k] = reinterpret_cast<const uint16_t*>(p.epi.residual)[static_cast<uint64_t>(t) * p.epi.ld_r + col];
+      }
+    };
+    auto finish_rows = [&](int c, auto sum) {
+#pragma unroll 1
+      for (int q = rank, slot = 0; q < C::kRedTok && sub0(c) + q < p.T; q += S, ++slot) {
+        const int t = sub0(c) + q;
+        float y = sum(slot);
+        if (MODE == kFewLinear) y = apply_act(y + bias, p.epi.act);
+        y += __uint_as_float(static_cast<uint32_t>(res[0]) << 16);
+#pragma unroll
+        for (int k = 0; k + 1 < C::kRedTok; ++k) res[k] = res[k + 1];
+        FGFP8_DCHECK(t < p.T && col < p.N);
+        p.Y[static_cast<uint64_t>(t) * p.N + col] = __float2bfloat16_rn(y);
+      }
+    };
+    if constexpr (MODE != kFewGateUp) {
+      load_res(0);
+      if (MODE == kFewLinear) bias = load_bias(p.epi, col);
+    }
+
     float acc[C::kChunks][C::kTiles][16];
     while (ok && work.next(sg)) {
-      const uint64_t m = tokens_of(sg);
-      const int n = __popcll(m);
+      const int n = count_of(sg), pair0 = pair0_of(sg);
 #pragma unroll
       for (int q = 0; q < C::kChunks; ++q)
 #pragma unroll
@@ -736,62 +802,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       }
       if (!ok) break;
 
-      if constexpr (MODE != kFewDown) {
-        if (S > 1) {
-#pragma unroll
-          for (int q = 0; q < C::kChunks; ++q)
-            if (chunk0(q) < n && ok) meet(acc[q], chunk0(q), n);
-          if (!ok) break;
-        }
-      }
-      if constexpr (MODE == kFewGateUp) {
-        // h = silu(g) u in fp32, its 1x128 group (the 128 threads' rows)
-        // quantized straight from fp32: no rounding to bf16 on the way
-        float* am = sAmax + (segs & 1u) * 4 * NT;
-#pragma unroll
-        for (int q = 0; q < C::kChunks; ++q) {
-          if (chunk0(q) >= n) break;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int ti = chunk0(q) + i;
-            if (ti < n && (i & (S - 1)) == rank) {
-              const float g = acc[q][0][i];
-              const float h = __fdiv_rn(g, 1.0f + expf(-g)) * acc[q][1][i];
-              acc[q][0][i] = h;
-              const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
-              if (lane == 0) am[quad * NT + ti] = __uint_as_float(top);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&amax_bar[grp]);
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&amax_bar[grp], segs & 1u))) {
-          expired();
-          break;
-        }
-        const uint64_t pair0 = sBase[sg.a];
-#pragma unroll
-        for (int q = 0; q < C::kChunks; ++q) {
-          if (chunk0(q) >= n) break;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int ti = chunk0(q) + i;
-            if (ti < n && (i & (S - 1)) == rank) {
-              // magnitude bits compare like the values, and a NaN above all of them
-              const uint32_t a01 = max(__float_as_uint(am[ti]), __float_as_uint(am[NT + ti]));
-              const uint32_t a23 = max(__float_as_uint(am[2 * NT + ti]), __float_as_uint(am[3 * NT + ti]));
-              const float scale = scale_of_f32(__uint_as_float(max(a01, a23)), p.fmt);
-              const uint64_t r = pair0 + ti;
-              FGFP8_DCHECK(r < static_cast<uint64_t>(p.T) * p.topk && sg.j * 128 + row < p.I);
-              p.Hq[r * p.I + sg.j * 128 + row] =
-                  __nv_cvt_float_to_fp8(__fdiv_rn(acc[q][0][i], scale), __NV_SATFINITE, __NV_E4M3);
-              if (row == 0) p.Hs[r * (p.I / 128) + sg.j] = scale;
-            }
-          }
-        }
-      } else if constexpr (MODE == kFewDown) {
-        // the expert's tokens, weighted, into the block's fp32 sums; a token
-        // that names the expert in several slots adds their weights.  The
+      if constexpr (MODE == kFewDown) {
+        // the expert's tokens, weighted, into the block's fp32 sums.  The
         // groups hold different tokens of one expert, but a token may change
         // groups from one expert to the next: each expert waits for the last.
         if (C::kGroups > 1 && segs > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(seg_bar, (segs - 1) & 1u))) {
@@ -801,18 +813,15 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
 #pragma unroll
         for (int q = 0; q < C::kChunks; ++q) {
           if (chunk0(q) >= n) break;
-          int tok = 0;
-          float wt = 0.0f;
-          if (lane < 16 && chunk0(q) + lane < n) {
-            tok = nth_bit(m, chunk0(q) + lane);
-            for (int k = 0; k < p.topk; ++k)
-              if (sIds[tok * p.topk + k] == sg.e) wt += sWt[tok * p.topk + k];
-          }
+          const int at = pair0 + chunk0(q) + lane;
+          const bool in = lane < 16 && chunk0(q) + lane < n;
+          const int tok = in ? sTok[at] : 0;
+          const float wt = in ? sWt[at] : 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int t = __shfl_sync(0xFFFFFFFFu, tok, i);
-            const float w = __shfl_sync(0xFFFFFFFFu, wt, i);
-            if (chunk0(q) + i < n) sAcc[t * 128 + row] = __fmaf_rn(w, acc[q][0][i], sAcc[t * 128 + row]);
+            if (chunk0(q) + i >= n) break;
+            float* to = sAcc + __shfl_sync(0xFFFFFFFFu, tok, i) * 128 + row;
+            *to = __fmaf_rn(__shfl_sync(0xFFFFFFFFu, wt, i), acc[q][0][i], *to);
           }
         }
         if (C::kGroups > 1) {
@@ -820,22 +829,58 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           if (lane == 0) mbar_arrive(seg_bar);
         }
       } else {
-        const int col = sg.j * 128 + row;
-        const float bias = load_bias(p.epi, col);
+        // a rolled loop over the meetings, so that the epilogue's code stays
+        // small: it runs once per 128 columns, from a cold instruction cache
+#pragma unroll 1
+        for (int c = 0; c < kSubs && sub0(c) < n; ++c) {
 #pragma unroll
-        for (int q = 0; q < C::kChunks; ++q) {
-          if (chunk0(q) >= n) break;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int t = chunk0(q) + i;
-            if (t < n && (i & (S - 1)) == rank) {
-              float y = apply_act(acc[q][0][i] + bias, p.epi.act);
-              if (p.epi.residual) y += __bfloat162float(p.epi.residual[static_cast<uint64_t>(t) * p.epi.ld_r + col]);
-              FGFP8_DCHECK(t < p.T && col < p.N);
-              p.Y[static_cast<uint64_t>(t) * p.N + col] = __float2bfloat16_rn(y);
+          for (int cc = 0; cc < kSubs; ++cc)
+            if (cc == c)
+              meet_put(n - sub0(c), [&](int q, int t) {
+                const int i = cc * C::kRedTok + q;
+                return acc[i / 16][t][i % 16];
+              });
+          if (!ok) break;
+          if constexpr (MODE == kFewLinear) {
+            if (c > 0) load_res(c);
+            finish_rows(c, [&](int slot) { return sum_of(slot, 0); });
+          } else {
+            // h = silu(g) u in fp32, its 1x128 group (the 128 threads' rows)
+            // quantized straight from fp32: no rounding to bf16 on the way
+            const int own = (n - sub0(c) < C::kRedTok ? n - sub0(c) : C::kRedTok);   // tokens of this meeting
+            if (rank < own) {
+              float* am = sAmax + (grp * 2 + (quants & 1u)) * 4 * C::kRedTok;
+#pragma unroll 1
+              for (int q = rank, slot = 0; q < own; q += S, ++slot) {
+                const float g = sum_of(slot, 0), u = sum_of(slot, 1);
+                const float h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
+                red[slot * C::kTiles * 128 + row] = h;       // read back by this thread alone
+                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
+                if (lane == 0) am[slot * 4 + quad] = __uint_as_float(top);
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&amax_bar[grp]);
+              if (!__all_sync(0xFFFFFFFFu, mbar_wait(&amax_bar[grp], quants & 1u))) {
+                expired();
+                break;
+              }
+              ++quants;
+#pragma unroll 1
+              for (int q = rank, slot = 0; q < own; q += S, ++slot) {
+                // magnitude bits compare like the values, and a NaN above all of them
+                const uint32_t* m4 = reinterpret_cast<const uint32_t*>(am) + slot * 4;
+                const float scale = scale_of_f32(__uint_as_float(max(max(m4[0], m4[1]), max(m4[2], m4[3]))), p.fmt);
+                const uint64_t r = static_cast<uint64_t>(pair0 + sub0(c) + q);
+                FGFP8_DCHECK(r < static_cast<uint64_t>(p.T) * p.topk && sg.j * 128 + row < p.I);
+                p.Hq[r * p.I + sg.j * 128 + row] = __nv_cvt_float_to_fp8(
+                    __fdiv_rn(red[slot * C::kTiles * 128 + row], scale), __NV_SATFINITE, __NV_E4M3);
+                if (row == 0) p.Hs[r * (p.I / 128) + sg.j] = scale;
+              }
             }
           }
+          meet_done();
         }
+        if (!ok) break;
       }
       ++segs;
     }
@@ -843,25 +888,14 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     if constexpr (MODE == kFewDown) {
       // the block's sums over all experts, residual added, one rounding
       if (C::kGroups > 1 && ok && segs > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(seg_bar, (segs - 1) & 1u))) expired();
-      const int col = cluster * 128 + row;
-#pragma unroll
-      for (int q = 0; q < C::kChunks; ++q) {
-        if (chunk0(q) >= p.T || !ok) break;
-        float val[1][16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) val[0][i] = sAcc[(chunk0(q) + i) * 128 + row];
-        if (S > 1) meet(val, chunk0(q), p.T);
+#pragma unroll 1
+      for (int c = 0; c < kSubs && sub0(c) < p.T && ok; ++c) {
+        const float* from = sAcc + sub0(c) * 128 + row;
+        if (S > 1) meet_put(p.T - sub0(c), [&](int q, int) { return from[q * 128]; });
         if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = chunk0(q) + i;
-          if (t < p.T && (i & (S - 1)) == rank) {
-            float y = val[0][i];
-            if (p.epi.residual) y += __bfloat162float(p.epi.residual[static_cast<uint64_t>(t) * p.epi.ld_r + col]);
-            FGFP8_DCHECK(col < p.N);
-            p.Y[static_cast<uint64_t>(t) * p.N + col] = __float2bfloat16_rn(y);
-          }
-        }
+        if (c > 0) load_res(c);
+        finish_rows(c, [&](int slot) { return S > 1 ? sum_of(slot, 0) : from[slot * 128]; });
+        meet_done();
       }
     }
   }
