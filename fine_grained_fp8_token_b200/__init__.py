@@ -398,74 +398,92 @@ def gemm_swiglu_quant(Xq, Xs, Wq_gu, Ws_gu, Hq=None, Hs=None, ld_h: int | None =
 # ---------------------------------------------------------------- epilogue, router, expert layer
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_ACT_CODES = frozenset(_ACTS.values())
 _SCORES = {"softmax": 0, "sigmoid": 1}
 FUSED_QUANT_TOKENS = 16       # linear_epilogue needs no Xq / Xs up to this many tokens
 MOE_MAX_TOKENS = 64
 
 
-def _need(ok: bool, where: str, message: str, status: int = 1) -> None:
-    if not ok:
-        raise FGFP8Error(status, where, message)
+_t = None                     # torch, imported with the first call
 
 
-def _matrix(t, where: str, name: str, dtype, device) -> int:
-    """Checks a row-major matrix operand; returns its row stride."""
-    _need(t.dtype == dtype and t.dim() == 2 and t.device == device, where,
-          f"{name} must be a {dtype} matrix on {device}")
+def _torch():
+    global _t
+    if _t is None:
+        import torch
+        _t = torch
+    return _t
+
+
+def _refuse(where: str, message: str, status: int = 1):
+    raise FGFP8Error(status, where, message)
+
+
+# The checks run on every call, so they build no message until one is needed.
+def _matrix(t, where: str, name: str, dtype, dev: int) -> int:
+    """Checks a row-major matrix operand on device index dev; returns its row
+    stride."""
+    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev:
+        _refuse(where, f"{name} must be a {dtype} matrix on device {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
     R, C = t.shape
     if R <= 1:
         return C                  # the stride of a single row says nothing
-    _need(t.stride(1) == 1 or C <= 1, where, f"{name} must have unit stride along its rows")
-    return t.stride(0)
+    ld, unit = t.stride()
+    if unit != 1 and C > 1:
+        _refuse(where, f"{name} must have unit stride along its rows")
+    return ld
 
 
-def _dense(t, where: str, name: str, dtype, shape, device) -> None:
-    ok = (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype)
-    _need(ok and tuple(t.shape) == shape and t.is_contiguous() and t.device == device, where,
-          f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+def _dense(t, where: str, name: str, dtypes, shape, dev: int) -> None:
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(where, f"{name} must be a contiguous {' or '.join(map(str, dtypes))} tensor of shape {tuple(shape)} on "
+                       f"device {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _codes_dtypes():
-    import torch
-    return torch.uint8, torch.float8_e4m3fn
+def _check_weight(Wq, Ws, where, fmt, dev, names=("Wq", "Ws"), dims=2):
+    """Checks a stack of block-quantized weights; returns its shape."""
+    t = _t
+    if fmt != SCALE_F32 and fmt != SCALE_UE8M0:
+        _refuse(where, "fmt must be SCALE_F32 (0) or SCALE_UE8M0 (1)")
+    shape = Wq.shape
+    if len(shape) != dims or shape[-1] % 128 or shape[-2] % 128:
+        _refuse(where, f"{names[0]} must have {dims} dimensions, the last two multiples of 128", 2)
+    _dense(Wq, where, names[0], (t.uint8, t.float8_e4m3fn), shape, dev)
+    _dense(Ws, where, names[1], (t.float32,) if fmt == SCALE_F32 else (t.uint8,),
+           (*shape[:-2], shape[-2] // 128, shape[-1] // 128), dev)
+    return shape
 
 
-def _check_weight(Wq, Ws, where, fmt, device, names=("Wq", "Ws"), lead=()):
-    _need(fmt in (SCALE_F32, SCALE_UE8M0), where, "fmt must be SCALE_F32 (0) or SCALE_UE8M0 (1)")
-    shape = tuple(Wq.shape)
-    _need(len(shape) == 2 + len(lead) and shape[-1] % 128 == 0 and shape[-2] % 128 == 0, where,
-          f"{names[0]} must be [{', '.join([*lead, 'N', 'K'])}] with N and K multiples of 128", 2)
-    _dense(Wq, where, names[0], _codes_dtypes(), shape, device)
-    _dense(Ws, where, names[1], _scale_dtype(fmt), shape[:-2] + (shape[-2] // 128, shape[-1] // 128), device)
-
-
-def _run_on(device, stream, where: str, call):
-    """call(stream handle) with `device` current; what it allocates belongs to
-    the stream it launches on."""
-    import torch
-    _need(device.type == "cuda", where, "the tensors must be on a CUDA device")
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(torch._C._cuda_getCurrentRawStream(device.index))
-    with torch.cuda.device(device):
+def _run_on(dev: int, stream, where: str, call):
+    """call(stream handle) with device index `dev` current; what it allocates
+    belongs to the stream it launches on."""
+    if dev < 0:
+        _refuse(where, "the tensors must be on a CUDA device")
+    cuda = _t.cuda
+    if stream is None and dev == cuda.current_device():
+        return call(_t._C._cuda_getCurrentRawStream(dev))
+    with cuda.device(dev):
         if stream is None:
-            return call(torch._C._cuda_getCurrentRawStream(device.index))
-        _need(stream.device == device, where, f"the stream must be on {device}")
-        with torch.cuda.stream(stream):
+            return call(_t._C._cuda_getCurrentRawStream(dev))
+        if stream.device.index != dev:
+            _refuse(where, f"the stream must be on device {dev}")
+        with cuda.stream(stream):
             return call(int(stream.cuda_stream))
 
 
-def _epilogue_args(where, M, N, device, bias, act, residual):
-    import torch
-    _need(act in _ACTS if isinstance(act, str) else act in _ACTS.values(), where,
-          f"act must be one of {sorted(_ACTS)} or its code")
-    code = _ACTS[act] if isinstance(act, str) else act
+def _epilogue_args(where, M, N, dev, bias, act, residual):
+    t = _t
+    code = _ACTS.get(act) if isinstance(act, str) else act
+    if code not in _ACT_CODES:
+        _refuse(where, f"act must be one of {sorted(_ACTS)} or its code")
     bp, bt, rp, ld_r = None, 0, None, N
     if bias is not None:
-        _dense(bias, where, "bias", (torch.bfloat16, torch.float32), (N,), device)
-        bp, bt = bias.data_ptr(), int(bias.dtype == torch.float32)
+        _dense(bias, where, "bias", (t.bfloat16, t.float32), (N,), dev)
+        bp, bt = bias.data_ptr(), int(bias.dtype is t.float32)
     if residual is not None:
-        ld_r = _matrix(residual, where, "residual", torch.bfloat16, device)
-        _need(tuple(residual.shape) == (M, N), where, f"residual must be [{M}, {N}]", 2)
+        ld_r = _matrix(residual, where, "residual", t.bfloat16, dev)
+        if residual.shape != (M, N):
+            _refuse(where, f"residual must be [{M}, {N}]", 2)
         rp = residual.data_ptr()
     return bp, bt, code, rp, ld_r
 
@@ -473,22 +491,26 @@ def _epilogue_args(where, M, N, device, bias, act, residual):
 def gemm_epilogue(Xq, Xs, Wq, Ws, fmt: int, bias=None, act="none", residual=None, Y=None, stream=None):
     """Y = bf16(act(X W^T + bias) + residual) from the quantized operands
     (Xq uint8 [M, K], Xs [K/128, ld_s], Wq [N, K], Ws [N/128, K/128]); bias [N]
-    bf16 or fp32, residual bf16 [M, N] with any row stride (it may be Y), act
-    one of none, relu, silu, gelu, gelu_tanh.  Returns Y."""
-    import torch
-    where, dev = "gemm_epilogue", Xq.device
-    _check_weight(Wq, Ws, where, fmt, dev)
-    (M, K), N = Xq.shape, Wq.shape[0]
-    _dense(Xq, where, "Xq", _codes_dtypes(), (M, Wq.shape[1]), dev)
-    _dense(Xs, where, "Xs", _scale_dtype(fmt), (K // 128, Xs.shape[-1]), dev)
+    bf16 or fp32, residual bf16 [M, N] with any row stride that is a multiple
+    of 8 (it may be Y), act one of none, relu, silu, gelu, gelu_tanh.  Returns
+    Y."""
+    where, t = "gemm_epilogue", _torch()
+    dev = Xq.get_device()
+    N, K = _check_weight(Wq, Ws, where, fmt, dev)
+    M = Xq.shape[0]
+    _dense(Xq, where, "Xq", (t.uint8, t.float8_e4m3fn), (M, K), dev)
+    _dense(Xs, where, "Xs", (t.float32,) if fmt == SCALE_F32 else (t.uint8,), (K // 128, Xs.shape[-1]), dev)
     epi = _epilogue_args(where, M, N, dev, bias, act, residual)
     if Y is not None:
-        _dense(Y, where, "Y", torch.bfloat16, (M, N), dev)
+        _dense(Y, where, "Y", (t.bfloat16,), (M, N), dev)
+    lib = load()
 
     def call(s):
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if Y is None else Y
-        _check(fgfp8_gemm_epilogue(Xq.data_ptr(), Xs.data_ptr(), Xs.shape[1], Wq.data_ptr(), Ws.data_ptr(),
-                                   out.data_ptr(), M, N, K, fmt, *epi, s), "fgfp8_gemm_epilogue")
+        out = Xq.new_empty((M, N), dtype=t.bfloat16) if Y is None else Y
+        st = lib.fgfp8_gemm_epilogue(Xq.data_ptr(), Xs.data_ptr(), Xs.shape[1], Wq.data_ptr(), Ws.data_ptr(),
+                                     out.data_ptr(), M, N, K, fmt, *epi, s)
+        if st:
+            _check(st, "fgfp8_gemm_epilogue")
         return out
     return _run_on(dev, stream, where, call)
 
@@ -500,32 +522,37 @@ def linear_epilogue(X, Wq, Ws, fmt: int, bias=None, act="none", residual=None, Y
     the pre-quantized weight.  Xq / Xs are the quantizer's buffers (allocated
     here when not given, not needed for M <= FUSED_QUANT_TOKENS); bias, act and
     residual as in gemm_epilogue.  Returns Y."""
-    import torch
-    where, dev = "linear_epilogue", X.device
-    _check_weight(Wq, Ws, where, fmt, dev)
-    ldx = _matrix(X, where, "X", torch.bfloat16, dev)
-    (M, K), N = X.shape, Wq.shape[0]
-    _need(K == Wq.shape[1], where, f"X has {K} columns, Wq {Wq.shape[1]}", 2)
+    where, t = "linear_epilogue", _torch()
+    dev = X.get_device()
+    N, K = _check_weight(Wq, Ws, where, fmt, dev)
+    ldx = _matrix(X, where, "X", t.bfloat16, dev)
+    M = X.shape[0]
+    if X.shape[1] != K:
+        _refuse(where, f"X has {X.shape[1]} columns, Wq {K}", 2)
     epi = _epilogue_args(where, M, N, dev, bias, act, residual)
     if Y is not None:
-        _dense(Y, where, "Y", torch.bfloat16, (M, N), dev)
-    if Xq is not None:
-        _dense(Xq, where, "Xq", _codes_dtypes(), (M, K), dev)
+        _dense(Y, where, "Y", (t.bfloat16,), (M, N), dev)
     ld = scale_rows(M, fmt) if ld_s is None else ld_s
+    sdtype = t.float32 if fmt == SCALE_F32 else t.uint8
+    if Xq is not None:
+        _dense(Xq, where, "Xq", (t.uint8, t.float8_e4m3fn), (M, K), dev)
     if Xs is not None:
-        _dense(Xs, where, "Xs", _scale_dtype(fmt), (K // 128, ld), dev)
+        _dense(Xs, where, "Xs", (sdtype,), (K // 128, ld), dev)
+    lib = load()
 
     def call(s):
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if Y is None else Y
+        out = X.new_empty((M, N)) if Y is None else Y
         q, sc = Xq, Xs
         if M > FUSED_QUANT_TOKENS:
             if q is None:
-                q = torch.empty((M, K), dtype=torch.uint8, device=dev)
+                q = X.new_empty((M, K), dtype=t.uint8)
             if sc is None:
-                sc = torch.empty((K // 128, ld), dtype=_scale_dtype(fmt), device=dev)
-        _check(fgfp8_linear_epilogue(X.data_ptr(), ldx, None if q is None else q.data_ptr(),
-                                     None if sc is None else sc.data_ptr(), ld, Wq.data_ptr(), Ws.data_ptr(),
-                                     out.data_ptr(), M, N, K, fmt, *epi, s), "fgfp8_linear_epilogue")
+                sc = X.new_empty((K // 128, ld), dtype=sdtype)
+        st = lib.fgfp8_linear_epilogue(X.data_ptr(), ldx, None if q is None else q.data_ptr(),
+                                       None if sc is None else sc.data_ptr(), ld, Wq.data_ptr(), Ws.data_ptr(),
+                                       out.data_ptr(), M, N, K, fmt, *epi, s)
+        if st:
+            _check(st, "fgfp8_linear_epilogue")
         return out
     return _run_on(dev, stream, where, call)
 
@@ -537,27 +564,33 @@ def route_topk(logits, topk: int, score: str = "softmax", bias=None, n_group: in
     selection bias [E]; the topk_group best of n_group groups compete.
     Experts at -inf or NaN are never chosen; empty slots hold id -1 and
     weight 0.  Returns (ids int32 [T, topk], weights fp32 [T, topk])."""
-    import torch
-    where, dev = "route_topk", logits.device
-    _need(logits.dtype in (torch.bfloat16, torch.float32), where, "logits must be bf16 or fp32")
-    ld = _matrix(logits, where, "logits", logits.dtype, dev)
+    where, t = "route_topk", _torch()
+    dev = logits.get_device()
+    dtype = logits.dtype
+    if dtype is not t.float32 and dtype is not t.bfloat16:
+        _refuse(where, "logits must be bf16 or fp32")
+    ld = _matrix(logits, where, "logits", dtype, dev)
     T, E = logits.shape
-    _need(score in _SCORES, where, f"score must be one of {sorted(_SCORES)}")
+    if score not in _SCORES:
+        _refuse(where, f"score must be one of {sorted(_SCORES)}")
+    if topk < 1:
+        _refuse(where, "topk must be at least 1", 2)
     if bias is not None:
-        _dense(bias, where, "bias", torch.float32, (E,), dev)
+        _dense(bias, where, "bias", (t.float32,), (E,), dev)
     if ids is not None:
-        _dense(ids, where, "ids", torch.int32, (T, topk), dev)
+        _dense(ids, where, "ids", (t.int32,), (T, topk), dev)
     if weights is not None:
-        _dense(weights, where, "weights", torch.float32, (T, topk), dev)
-    _need(topk >= 1, where, "topk must be at least 1", 2)
+        _dense(weights, where, "weights", (t.float32,), (T, topk), dev)
+    lib = load()
 
     def call(s):
-        i = torch.empty((T, topk), dtype=torch.int32, device=dev) if ids is None else ids
-        w = torch.empty((T, topk), dtype=torch.float32, device=dev) if weights is None else weights
-        _check(fgfp8_route_topk(logits.data_ptr(), int(logits.dtype == torch.float32), ld,
-                                None if bias is None else bias.data_ptr(), T, E, topk, _SCORES[score], n_group,
-                                topk_group, int(renormalize), scale, i.data_ptr(), w.data_ptr(), s),
-               "fgfp8_route_topk")
+        i = logits.new_empty((T, topk), dtype=t.int32) if ids is None else ids
+        w = logits.new_empty((T, topk), dtype=t.float32) if weights is None else weights
+        st = lib.fgfp8_route_topk(logits.data_ptr(), int(dtype is t.float32), ld,
+                                  None if bias is None else bias.data_ptr(), T, E, topk, _SCORES[score], n_group,
+                                  topk_group, int(renormalize), scale, i.data_ptr(), w.data_ptr(), s)
+        if st:
+            _check(st, "fgfp8_route_topk")
         return i, w
     return _run_on(dev, stream, where, call)
 
@@ -577,37 +610,40 @@ def moe_decode(X, ids, weights, W13q, W13s, W2q, W2s, fmt: int, residual=None, Y
     Y[t] = bf16(residual[t] + sum_j weights[t, j] expert_{ids[t, j]}(X[t])).
     workspace: uint8 tensor of moe_workspace_bytes(T, topk, I) (allocated here
     when not given; calls that may overlap need their own).  Returns Y."""
-    import torch
-    where, dev = "moe_decode", X.device
-    _check_weight(W13q, W13s, where, fmt, dev, ("W13q", "W13s"), ("E",))
-    _check_weight(W2q, W2s, where, fmt, dev, ("W2q", "W2s"), ("E",))
-    ldx = _matrix(X, where, "X", torch.bfloat16, dev)
-    T, K = X.shape
-    E, I = W13q.shape[0], W2q.shape[2]
-    _need(tuple(W13q.shape) == (E, 2 * I, K) and tuple(W2q.shape) == (E, K, I), where,
-          "W13q must be [E, 2I, K] and W2q [E, K, I] with X [T, K]", 2)
-    _need(ids.dim() == 2, where, "ids must be [T, topk]", 2)
+    where, t = "moe_decode", _torch()
+    dev = X.get_device()
+    s13 = _check_weight(W13q, W13s, where, fmt, dev, ("W13q", "W13s"), 3)
+    E, K, I = _check_weight(W2q, W2s, where, fmt, dev, ("W2q", "W2s"), 3)
+    ldx = _matrix(X, where, "X", t.bfloat16, dev)
+    T = X.shape[0]
+    if X.shape[1] != K or s13 != (E, 2 * I, K):
+        _refuse(where, "W13q must be [E, 2I, K] and W2q [E, K, I] with X [T, K]", 2)
+    if ids.dim() != 2:
+        _refuse(where, "ids must be [T, topk]", 2)
     topk = ids.shape[1]
-    _dense(ids, where, "ids", torch.int32, (T, topk), dev)
-    _dense(weights, where, "weights", torch.float32, (T, topk), dev)
+    _dense(ids, where, "ids", (t.int32,), (T, topk), dev)
+    _dense(weights, where, "weights", (t.float32,), (T, topk), dev)
     rp, ld_r = None, K
     if residual is not None:
-        ld_r = _matrix(residual, where, "residual", torch.bfloat16, dev)
-        _need(tuple(residual.shape) == (T, K), where, f"residual must be [{T}, {K}]", 2)
+        ld_r = _matrix(residual, where, "residual", t.bfloat16, dev)
+        if residual.shape != (T, K):
+            _refuse(where, f"residual must be [{T}, {K}]", 2)
         rp = residual.data_ptr()
     if Y is not None:
-        _dense(Y, where, "Y", torch.bfloat16, (T, K), dev)
+        _dense(Y, where, "Y", (t.bfloat16,), (T, K), dev)
+    need = moe_workspace_bytes(T, topk, I)
     if workspace is not None:
-        _dense(workspace, where, "workspace", torch.uint8, (workspace.numel(),), dev)
+        _dense(workspace, where, "workspace", (t.uint8,), (workspace.numel(),), dev)
+    lib = load()
 
     def call(s):
-        out = torch.empty((T, K), dtype=torch.bfloat16, device=dev) if Y is None else Y
-        ws = workspace
-        if ws is None:
-            ws = torch.empty((moe_workspace_bytes(T, topk, I),), dtype=torch.uint8, device=dev)
-        _check(fgfp8_moe_decode(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), W13q.data_ptr(),
-                                W13s.data_ptr(), W2q.data_ptr(), W2s.data_ptr(), rp, ld_r, out.data_ptr(),
-                                ws.data_ptr(), ws.numel(), T, topk, E, K, I, fmt, s), "fgfp8_moe_decode")
+        out = X.new_empty((T, K)) if Y is None else Y
+        ws = X.new_empty((need,), dtype=t.uint8) if workspace is None else workspace
+        st = lib.fgfp8_moe_decode(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), W13q.data_ptr(),
+                                  W13s.data_ptr(), W2q.data_ptr(), W2s.data_ptr(), rp, ld_r, out.data_ptr(),
+                                  ws.data_ptr(), ws.numel(), T, topk, E, K, I, fmt, s)
+        if st:
+            _check(st, "fgfp8_moe_decode")
         return out
     return _run_on(dev, stream, where, call)
 

@@ -1237,10 +1237,14 @@ fgfp8_status fgfp8_route_topk(const void* logits, int logits_type, int64_t ld, c
   a.logits = logits;
   a.ld = static_cast<uint64_t>(ld);
   a.bias = bias;
+  a.vec = aligned(logits, 16) && aligned(bias, 16) && ld * (logits_type == FGFP8_F32 ? 4 : 2) % 16 == 0;
   a.T = static_cast<int>(T);
   a.E = static_cast<int>(E);
   a.topk = static_cast<int>(topk);
   a.n_group = static_cast<int>(n_group);
+  a.group_lanes = 5;
+  while ((32 >> a.group_lanes) < a.n_group) --a.group_lanes;
+  a.per = fgfp8::FastDiv(static_cast<uint32_t>(E / n_group));
   a.topk_group = static_cast<int>(topk_group);
   a.renormalize = renormalize;
   a.scale = scale;

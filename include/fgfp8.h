@@ -270,7 +270,9 @@ fgfp8_status fgfp8_linear_epilogue(const void* X, int64_t ldx, uint8_t* Xq, void
  *            elements (ld >= E).
  *   score    FGFP8_ROUTE_SOFTMAX: key_e = z_e, p = softmax(z) over all E;
  *            FGFP8_ROUTE_SIGMOID: key_e = sigmoid(z_e) + bias_e, p_e =
- *            sigmoid(z_e).  Sigmoid keys are formed and compared in 64 bits.
+ *            sigmoid(z_e).  Sigmoid keys and group scores are compared as in
+ *            64 bits; without a bias the logits themselves are compared, as
+ *            they have the same order.
  *   bias     float [E], only for the selection and only with sigmoid scores;
  *            NULL: none.
  *   n_group, topk_group  the experts form n_group runs of E / n_group; a

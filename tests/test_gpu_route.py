@@ -58,6 +58,8 @@ def reference(z, topk, score, bias, G, keep, renorm, scale):
             for g in range(G):
                 if g not in best:
                     key[g * per:(g + 1) * per] = -np.inf
+        if bias is None:                             # the logits' order is the sigmoids' in exact arithmetic
+            key = np.where(key > -np.inf, z[t], -np.inf)
         order = sorted(range(E), key=lambda e: (-key[e], e))[:topk]
         chosen = [e for e in order if key[e] > -np.inf]
         total = max(sum(p[e] for e in chosen), 1e-20) if renorm else 1.0
@@ -124,6 +126,10 @@ def test_masks_ties_and_infinities(dev, score, G, keep):
     z[8] = (z[8] * 2).round() / 2                    # many ties
     z[9, 5] = 80.0
     z[10] = z[10] - 60
+    z[13] = z[13] - 1000                             # sigmoids that vanish in 32 bits, and in 64
+    z[14] = 0.0
+    z[14, ::3] = -0.0                                # the two zeros are equal
+    z[15] = z[15] * 0.01 + 40                        # sigmoids that are 1 in 64 bits
     check(dev, z, topk, score=score, G=G, keep=keep)
     if score == "sigmoid":
         b = torch.zeros(E)
@@ -149,6 +155,17 @@ def test_near_ties_in_64_bits(dev):
     check(dev, z, 8, score="sigmoid")
     check(dev, z, 8, score="sigmoid", bias=torch.full((32,), 0.25))
     check(dev, z, 8, score="sigmoid", bias=torch.full((32,), 0.25), G=4, keep=2)
+    # more close keys than a warp has lanes, distinct and equal ones
+    for E, G, keep in ((40, 1, 1), (256, 8, 4), (512, 4, 2)):
+        z = torch.full((6, E), 14.0)
+        for t in range(3):
+            z[t] += torch.randperm(E, generator=torch.Generator().manual_seed(t)) * 2.0 ** -20
+        z[4, 7:] = -math.inf
+        z[5, ::2] = -1.0
+        check(dev, z, 8, score="sigmoid", bias=torch.full((E,), 0.25))
+        check(dev, z, 8, score="sigmoid", bias=torch.full((E,), 0.25), G=G, keep=keep)
+        check(dev, z, 8, score="sigmoid", bias=torch.arange(E).flip(0) * 2.0 ** -40, G=G, keep=keep)
+        check(dev, z, 8, score="sigmoid", G=G, keep=keep)
 
 
 def test_strided_and_many_tokens(dev):
