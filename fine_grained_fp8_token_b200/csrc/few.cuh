@@ -82,6 +82,11 @@ struct FewCfg {
   static constexpr int kTiles = MODE == kFewGateUp ? 2 : 1;          // 128-row weight tiles per stage
   static constexpr uint32_t kABytes = kTiles * 128 * 128;
   static constexpr uint32_t kBBytes = NT * 128;
+  // The products sa * sw have a ring of their own, so that a stage is free as
+  // soon as its MMAs are done.  When a token warp may write block u's, the
+  // MMAs of block u - kStages are done, so the promotion has left the pair two
+  // before that block's, and with it every block up to u - kStages - 4.
+  static constexpr int kScSlots = MODE == kFewGateUp && NT == 16 ? 8 : 16;
   static constexpr uint32_t kScBytes = kTiles * NT * 4;
   // tokens per meeting of the ranks, and the largest cluster: its buffer
   // holds max(kRedTok, S) tokens
@@ -105,14 +110,14 @@ struct FewCfg {
   static constexpr uint32_t kTokBytes = kMoe ? kPairs : 0;                          // token of each pair, u8
   static constexpr uint32_t kWeightBytes = MODE == kFewDown ? kPairs * 4 : 0;       // weight of each pair
   static constexpr uint32_t kAmaxBytes = MODE == kFewGateUp ? kGroups * 2 * 4 * kRedTok * 4 : 0;
-  static constexpr uint32_t kBarrierBytes = NT == 64 ? 320 : 256;
+  static constexpr uint32_t kBarrierBytes = 384;
   // Two CTAs per SM while the token tile is small: one CTA's ramp and
   // epilogue run under the other's stream.
   static constexpr int kCtas = NT == 16 ? 2 : 1;
   static constexpr uint32_t kBudget = (kCtas == 2 ? 115712u : 232448u) - 1024u;     // after the 1 KB alignment
   static constexpr uint32_t kFixed =
-      kRedBytes + kAccBytes + kMaskBytes + kBaseBytes + kActBytes + kTokBytes + kWeightBytes + kAmaxBytes + kBarrierBytes;
-  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kScBytes;
+      kScSlots * kScBytes + kRedBytes + kAccBytes + kMaskBytes + kBaseBytes + kActBytes + kTokBytes + kWeightBytes + kAmaxBytes + kBarrierBytes;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
   static constexpr int kStagesFit = static_cast<int>((kBudget - kFixed) / kStageBytes);
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
   static constexpr size_t kSmemBytes = 1024 + kFixed + static_cast<size_t>(kStages) * kStageBytes;
@@ -121,14 +126,20 @@ struct FewCfg {
   // knows that block u - kTokWarps - kStages is consumed, and its parity
   // wait for block u tells phases apart only if that covers u - 2 kStages.
   static constexpr int kTokWarps = kStages < 4 ? kStages : 4;
-  static constexpr int kNumBuf = MODE == kFewGateUp && NT == 64 ? 2 : 4;             // TMEM partial buffers
-  static constexpr uint32_t kBufCols = kTiles * NT;
-  static constexpr uint32_t kTmemCols = kNumBuf * kBufCols;                          // 64, 128 or 256
+  // TMEM holds two pairs of K blocks: the promotion takes a pair at a time
+  // (one wait for the MMAs and one for the TMEM loads of both; with single
+  // blocks its chain of waits took 500 cycles a block, where 16 KB of weights
+  // take 540 to 700).
+  static constexpr int kNumBuf = 2;
+  static constexpr uint32_t kBlockCols = kTiles * NT;
+  static constexpr uint32_t kBufCols = 2 * kBlockCols;
+  static constexpr uint32_t kTmemCols = kNumBuf * kBufCols;                          // 64 to 512
   static constexpr int kThreads = (kEpiWarps + 6) * 32;
   static_assert(kStages >= 3, "pipeline depth");
+  static_assert(kScSlots >= kStages + 4, "ring of the scales");
   static_assert(kTokWarps <= kStages && kTokWarps <= 4, "parity waits of the token warps");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols * kCtas <= 512, "TMEM columns");
-  static_assert((2 * kStages + 2 * kNumBuf + 8) * 8 + 16 <= kBarrierBytes, "barrier area");
+  static_assert((2 * kStages + kScSlots + 2 * kNumBuf + 8) * 8 + 16 <= kBarrierBytes, "barrier area");
 };
 
 // ------------------------------------------------------------ cluster helpers
@@ -169,10 +180,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
   return true;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // ------------------------------------------------------------ scales
 // fp32 value of a stored scale: fp32 bits, or the power of two of a UE8M0
@@ -280,8 +289,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = sA + C::kStages * C::kABytes;
-  float* sSc = reinterpret_cast<float*>(sB + C::kStages * C::kBBytes);             // [stage][tile][NT]
-  float* sAcc = sSc + C::kStages * C::kTiles * NT;                                 // Down: [token][128]
+  float* sSc = reinterpret_cast<float*>(sB + C::kStages * C::kBBytes);             // [slot][tile][NT]
+  float* sAcc = sSc + C::kScSlots * C::kTiles * NT;                                // Down: [token][128]
   float* sRed = sAcc + C::kAccBytes / 4;                                           // [group][rank][slot][tile][128]
   Mask* sMask = reinterpret_cast<Mask*>(sRed + C::kRedBytes / 4);                  // tokens of each expert
   float* sWt = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sMask) + C::kMaskBytes);
@@ -295,7 +304,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   uint64_t* red_empty = red_full + 2;
   uint64_t* amax_bar = red_empty + 2;
   uint64_t* seg_bar = amax_bar + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_bar + 1);
+  uint64_t* sc_full = seg_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + C::kScSlots);
   uint16_t* sBase = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(full) + C::kBarrierBytes);
   uint16_t* sAct = sBase + C::kBaseBytes / 2;
   uint8_t* sTok = reinterpret_cast<uint8_t*>(sAct + C::kActBytes / 2);
@@ -310,8 +320,9 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1 + 1);                 // the TMA warp and the block's token warp
-      mbar_init(&empty[s], 1 + C::kEpiWarps);     // the MMAs and the promotion warps (scales)
+      mbar_init(&empty[s], 1);                    // the MMAs
     }
+    for (int s = 0; s < C::kScSlots; ++s) mbar_init(&sc_full[s], 1);
     for (int b = 0; b < C::kNumBuf; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], C::kEpiWarps);
@@ -337,10 +348,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   // CTAs then request weights while the last CTAs here finish.  For Down the
   // routing is complete before it starts (GateUp waited for it), so only H
   // and the output wait for GateUp.
-  if (MODE == kFewGateUp) {
-    griddep_wait();
-    griddep_launch_dependents();
-  }
+  if (MODE == kFewGateUp) griddep_wait();
+  griddep_launch_dependents();                    // the others' dependents wait before they touch memory
   int active = 1;
   if constexpr (kMoe) {
     // sMask[e]: the tokens routed to e; sAct: the experts with any, ascending;
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (S > 1) cluster_sync();                      // the ranks' barriers exist before anyone arrives on them
+  if (S > 1) cluster_arrive();                    // this CTA's barriers exist; the promotion warps wait for the others'
   const uint32_t tmem_base = *tmem_slot;
   FewIter<MODE> work(p, active, sAct, rank, cluster, clusters);
   FewSeg sg{};
@@ -447,34 +456,41 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     // ================= MMA issuer: the whole warp keeps the loop's state
     // uniform, one elected lane issues
     const uint64_t a_desc0 = smem_desc_k_sw128(smem_u32(sA)), b_desc0 = smem_desc_k_sw128(smem_u32(sB));
-    uint32_t it = 0;
+    uint32_t it = 0, pairs = 0;
     bool ok = true;
     while (ok && work.next(sg)) {
       const int n = __shfl_sync(0xFFFFFFFFu, (count_of(sg) + 15) & ~15, 0);
       const uint32_t idesc = idesc_e4m3_f32(128, n);
-      for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-        const int s = it % C::kStages, b = it % C::kNumBuf;
-        bool got = mbar_wait(&full[s], (it / C::kStages) & 1u);
-        if (it >= static_cast<uint32_t>(C::kNumBuf)) got = got && mbar_wait(&tempty[b], ((it / C::kNumBuf) & 1u) ^ 1u);
-        if (!__all_sync(0xFFFFFFFFu, got)) {
-          if (lane == 0) record_status(kDevTimeoutMma);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
+      for (int kb = sg.kb0; kb < sg.kb1 && ok; kb += 2, ++pairs) {
+        const int b = pairs % C::kNumBuf;
+        const int blocks = sg.kb1 - kb < 2 ? 1 : 2;
+        bool got = pairs < static_cast<uint32_t>(C::kNumBuf) || mbar_wait(&tempty[b], ((pairs / C::kNumBuf) & 1u) ^ 1u);
 #pragma unroll
-          for (int t = 0; t < C::kTiles; ++t) {
-            const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::kBufCols + t * NT);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8f6f4(d, a_desc0 + ((s * C::kABytes + t * 16384 + kk * 32) >> 4),
-                         b_desc0 + ((s * C::kBBytes + kk * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+        for (int h = 0; h < 2; ++h) {
+          if (h == blocks) break;
+          const int s = it % C::kStages;
+          got = got && mbar_wait(&full[s], (it / C::kStages) & 1u);
+          if (!__all_sync(0xFFFFFFFFu, got)) {
+            if (lane == 0) record_status(kDevTimeoutMma);
+            ok = false;
+            break;
           }
-          mma_commit(&empty[s]);
-          mma_commit(&tfull[b]);
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t) {
+              const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::kBufCols + h * C::kBlockCols + t * NT);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f8f6f4(d, a_desc0 + ((s * C::kABytes + t * 16384 + kk * 32) >> 4),
+                           b_desc0 + ((s * C::kBBytes + kk * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(&empty[s]);
+            if (h + 1 == blocks) mma_commit(&tfull[b]);
+          }
+          __syncwarp();
+          ++it;
         }
-        __syncwarp();
       }
     }
     if (elect_one()) mma_commit(mma_done);
@@ -511,8 +527,9 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
         // so that their loads and reductions overlap, or one for up to four
         // tokens.
         const int team = lane >> 3, l8 = lane & 7;
-        uint4 v[4][2];
-        auto load = [&](auto passes, int c, int kb) {
+        constexpr int kAhead = NT > 16 ? 2 : 1;                      // chunks in registers
+        uint4 v[kAhead][4][2];
+        auto load = [&](auto passes, uint4 (&v)[4][2], int c, int kb) {
           constexpr int P = decltype(passes)::value;
 #pragma unroll
           for (int q = 0; q < P; ++q) {
@@ -527,10 +544,9 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             }
           }
         };
-        auto store = [&](auto passes, auto fmt, int c, int s) {
+        auto store = [&](auto passes, auto fmt, const uint4 (&v)[4][2], int c, int s, float* sc) {
           constexpr int P = decltype(passes)::value, F = decltype(fmt)::value;
           uint8_t* tile = sB + s * C::kBBytes;
-          float* sc = sSc + s * C::kTiles * NT;
           uint32_t am[P];
 #pragma unroll
           for (int q = 0; q < P; ++q) am[q] = max(absmax_bits8(v[q][0]), absmax_bits8(v[q][1]));
@@ -560,25 +576,27 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
         };
         using One = std::integral_constant<int, 1>;
         using Four = std::integral_constant<int, 4>;
-        auto load16 = [&](int c, int kb) {
-          if (n - c * 16 > 4) load(Four{}, c, kb);
-          else load(One{}, c, kb);
+        auto load16 = [&](uint4 (&v)[4][2], int c, int kb) {
+          if (n - c * 16 > 4) load(Four{}, v, c, kb);
+          else load(One{}, v, c, kb);
         };
-        auto store16 = [&](int c, int s) {
+        auto store16 = [&](const uint4 (&v)[4][2], int c, int s, float* sc) {
           using F32 = std::integral_constant<int, 0>;
           using E8 = std::integral_constant<int, 1>;
           if (n - c * 16 > 4) {
-            if (p.fmt == 0) store(Four{}, F32{}, c, s);
-            else store(Four{}, E8{}, c, s);
+            if (p.fmt == 0) store(Four{}, F32{}, v, c, s, sc);
+            else store(Four{}, E8{}, v, c, s, sc);
           } else {
-            if (p.fmt == 0) store(One{}, F32{}, c, s);
-            else store(One{}, E8{}, c, s);
+            if (p.fmt == 0) store(One{}, F32{}, v, c, s, sc);
+            else store(One{}, E8{}, v, c, s, sc);
           }
         };
-        if (mine < it_end) {
-          load16(0, kb_of(mine));
-          load_sw(kb_of(mine));
-        }
+        auto load_first = [&](int kb) {
+          load16(v[0], 0, kb);
+          if (kAhead > 1 && n > 16) load16(v[kAhead - 1], 1, kb);
+          load_sw(kb);
+        };
+        if (mine < it_end) load_first(kb_of(mine));
         for (; mine < it_end; mine += C::kTokWarps) {
           const int kb = kb_of(mine);
           const int s = mine % C::kStages;
@@ -586,19 +604,22 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             ok = false;
             break;
           }
-          store16(0, s);
-#pragma unroll 1
-          for (int c = 1; c * 16 < n; ++c) {
-            load16(c, kb);
-            store16(c, s);
+          float* sc = sSc + (mine % C::kScSlots) * C::kTiles * NT;
+          store16(v[0], 0, s, sc);
+          if constexpr (kAhead > 1) {
+            if (n > 32) load16(v[0], 2, kb);
+            if (n > 16) store16(v[1], 1, s, sc);
+            if (n > 48) load16(v[1], 3, kb);
+            if (n > 32) store16(v[0], 2, s, sc);
+            if (n > 48) store16(v[1], 3, s, sc);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&full[s]);
-          if (mine + C::kTokWarps < it_end) {
-            load16(0, kb + C::kTokWarps);
-            load_sw(kb + C::kTokWarps);
+          if (lane == 0) {
+            mbar_arrive(&full[s]);
+            mbar_arrive(&sc_full[mine % C::kScSlots]);
           }
+          if (mine + C::kTokWarps < it_end) load_first(kb + C::kTokWarps);
         }
       } else {
         // lane: the scales of tokens lane, lane + 32; lane 0 requests the rows
@@ -629,7 +650,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             ok = false;
             break;
           }
-          float* sc = sSc + s * C::kTiles * NT;
+          float* sc = sSc + (mine % C::kScSlots) * C::kTiles * NT;
           const float w = scale_value(sw[0], p.fmt);
 #pragma unroll
           for (int q = 0; q < kTok; ++q) {
@@ -638,6 +659,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           }
           __syncwarp();
           if (lane == 0) {
+            mbar_arrive(&sc_full[mine % C::kScSlots]);
             mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n16 * 2048));
             for (int c = 0; c < n16; ++c)
               tma_load_2d(sB + s * C::kBBytes + c * 2048, &tmX, &full[s], kb * 128, pair0 + c * 16);
@@ -658,7 +680,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     float* red = sRed + grp * (C::kRedBytes / C::kGroups / 4);
     constexpr int kSubs = C::kChunks * 16 / C::kRedTok;              // meetings of a full tile
     const int slots = C::kRedTok >> lgS;                             // tokens of a meeting per rank
-    uint32_t it = 0, meets = 0, segs = 0, quants = 0;
+    uint32_t it = 0, pairs = 0, meets = 0, segs = 0, quants = 0;
     bool ok = true;
     auto expired = [&] {
       if (lane == 0) record_status(kDevTimeoutEpilogue);
@@ -667,76 +689,87 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     // first token of this group's chunk q, and of its meeting c
     auto chunk0 = [&](int q) { return (q * C::kGroups + grp) * 16; };
     auto sub0 = [&](int c) { return chunk0(c * C::kRedTok / 16) + c * C::kRedTok % 16; };
+    // A rank's token in slot k of a meeting is rank + k S (S divides kRedTok).
+    auto own_of = [&](int c, int n) {                                // slots with a token below n
+      const int left = n - sub0(c) - rank;
+      const int k = left <= 0 ? 0 : (left + S - 1) >> lgS;
+      return k < slots ? k : slots;
+    };
 
-    // One meeting of the ranks: each thread hands kRedTok tokens' partial sums
-    // of its row (val(q, t)) to the tokens' owners, token q to rank q % S
-    // (S divides kRedTok), slot q / S.  Between meet_put and meet_done the
-    // owner reads sum_of(slot, t), added in rank order.  Alone (S = 1) a
-    // thread meets only itself.
-    auto meet_put = [&](int count, auto val) {
-      if (S > 1 && meets > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_empty[grp], (meets - 1) & 1u))) {
+    // One meeting of the ranks: each thread's partial sums x of its row for
+    // kRedTok tokens, `count` of them real, go to the tokens' owners, token q
+    // to rank q % S, slot q / S; back come the sums over the ranks, added in
+    // rank order, of this rank's tokens in their slots.
+    auto meet = [&](float (&x)[C::kTiles][C::kRedTok], int count) {
+      if (meets == 0) cluster_wait();                                // the others' barriers exist
+      if (meets > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_empty[grp], (meets - 1) & 1u))) {
         expired();
         return;
       }
 #pragma unroll
       for (int q = 0; q < C::kRedTok; ++q) {
-        if (q < count) {
-          const int at = ((rank * slots + (q >> lgS)) * C::kTiles) * 128 + row;
-          if (S > 1) {
-            const uint32_t to = map_to_rank(smem_u32(red + at), q & (S - 1));
+        if (q >= count) break;
+        const int at = ((rank * slots + (q >> lgS)) * C::kTiles) * 128 + row;
+        const uint32_t to = map_to_rank(smem_u32(red + at), q & (S - 1));
 #pragma unroll
-            for (int t = 0; t < C::kTiles; ++t) st_cluster_f32(to + t * 512, val(q, t));
-          } else {
+        for (int t = 0; t < C::kTiles; ++t) st_cluster_f32(to + t * 512, x[t][q]);
+      }
+      __syncwarp();
+      if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_full[grp]), lane));
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_full[grp], meets & 1u))) {
+        expired();
+        return;
+      }
 #pragma unroll
-            for (int t = 0; t < C::kTiles; ++t) red[at + t * 128] = val(q, t);
+      for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+        for (int k = 0; k < C::kRedTok; ++k) x[t][k] = 0.0f;
+#pragma unroll 1
+      for (int r = 0; r < S; ++r) {
+        const float* from = red + r * slots * C::kTiles * 128 + row;
+#pragma unroll
+        for (int k = 0; k < C::kRedTok / 2; ++k)                     // S >= 2
+          if (k < slots) {
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t) x[t][k] += from[(k * C::kTiles + t) * 128];
           }
-        }
       }
-      if (S > 1) {
-        __syncwarp();
-        if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_full[grp]), lane));
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_full[grp], meets & 1u))) expired();
-      }
-    };
-    auto sum_of = [&](int slot, int t) {
-      float sum = 0.0f;
-      for (int r = 0; r < S; ++r) sum += red[((r * slots + slot) * C::kTiles + t) * 128 + row];
-      return sum;
-    };
-    auto meet_done = [&] {
-      if (S > 1) {
-        __syncwarp();
-        if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_empty[grp]), lane));
-        ++meets;
-      }
+      __syncwarp();
+      if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_empty[grp]), lane));
+      ++meets;
     };
 
-    // Output rows (Linear, Down): this rank's tokens of meeting c.  Their
+    // Output rows (Linear, Down): this rank's tokens of meeting c, all in
+    // flight together (one token after the other took 500 cycles each).  Their
     // residuals are loaded ahead: the first meeting's before the K loop.
     const int col = (MODE == kFewGateUp ? 0 : cluster) * 128 + row;
     float bias = 0.0f;
     uint16_t res[C::kRedTok];
     auto load_res = [&](int c) {
+      const int own = own_of(c, p.T);
+      const uint16_t* from = reinterpret_cast<const uint16_t*>(p.epi.residual) +
+                             static_cast<uint64_t>(sub0(c) + rank) * p.epi.ld_r + col;
 #pragma unroll
-      for (int k = 0; k < C::kRedTok; ++k) {
-        const int q = rank + (k << lgS), t = sub0(c) + q;
-        res[k] = 0;
-        if (p.epi.residual != nullptr && q < C::kRedTok && t < p.T)
-          res[k] = reinterpret_cast<const uint16_t*>(p.epi.residual)[static_cast<uint64_t>(t) * p.epi.ld_r + col];
-      }
+      for (int k = 0; k < C::kRedTok; ++k) res[k] = 0;
+      if (p.epi.residual == nullptr) return;
+#pragma unroll
+      for (int k = 0; k < C::kRedTok; ++k)
+        if (k < own) res[k] = from[(static_cast<uint64_t>(k) << lgS) * p.epi.ld_r];
     };
-    auto finish_rows = [&](int c, auto sum) {
-#pragma unroll 1
-      for (int q = rank, slot = 0; q < C::kRedTok && sub0(c) + q < p.T; q += S, ++slot) {
-        const int t = sub0(c) + q;
-        float y = sum(slot);
-        if (MODE == kFewLinear) y = apply_act(y + bias, p.epi.act);
-        y += __uint_as_float(static_cast<uint32_t>(res[0]) << 16);
+    auto finish_rows = [&](int c, float (&x)[C::kRedTok]) {
+      const int own = own_of(c, p.T);
+      if constexpr (MODE == kFewLinear) {
 #pragma unroll
-        for (int k = 0; k + 1 < C::kRedTok; ++k) res[k] = res[k + 1];
-        FGFP8_DCHECK(t < p.T && col < p.N);
-        p.Y[static_cast<uint64_t>(t) * p.N + col] = __float2bfloat16_rn(y);
+        for (int k = 0; k < C::kRedTok; ++k) x[k] += bias;
+        apply_act8(x, p.epi.act);
       }
+      FGFP8_DCHECK(col < p.N && (own == 0 || sub0(c) + rank + ((own - 1) << lgS) < p.T));
+      __nv_bfloat16* to = p.Y + static_cast<uint64_t>(sub0(c) + rank) * p.N + col;
+#pragma unroll
+      for (int k = 0; k < C::kRedTok; ++k)
+        if (k < own)
+          to[(static_cast<uint64_t>(k) << lgS) * p.N] =
+              __float2bfloat16_rn(x[k] + __uint_as_float(static_cast<uint32_t>(res[k]) << 16));
     };
     if constexpr (MODE != kFewGateUp) {
       load_res(0);
@@ -752,76 +785,82 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
         for (int t = 0; t < C::kTiles; ++t)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[q][t][i] = 0.0f;
-      for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-        const int b = it % C::kNumBuf, s = it % C::kStages;
-        // the scales come from other threads: the stage's full barrier orders them
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&full[s], (it / C::kStages) & 1u) &&
-                                         mbar_wait(&tfull[b], (it / C::kNumBuf) & 1u))) {
+      for (int kb = sg.kb0; kb < sg.kb1; kb += 2, ++pairs) {
+        const int b = pairs % C::kNumBuf;
+        const int blocks = sg.kb1 - kb < 2 ? 1 : 2;
+        const int s0 = it % C::kScSlots, s1 = (it + 1) % C::kScSlots;
+        bool got = mbar_wait(&tfull[b], (pairs / C::kNumBuf) & 1u) && mbar_wait(&sc_full[s0], (it / C::kScSlots) & 1u);
+        if (blocks == 2) got = got && mbar_wait(&sc_full[s1], ((it + 1) / C::kScSlots) & 1u);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
           expired();
           break;
         }
         tc_fence_after();
-        const float4* sc = reinterpret_cast<const float4*>(sSc + s * C::kTiles * NT);
-        // one wait for as many TMEM loads as registers allow
-        constexpr int kBatch = C::kTiles == 1 ? C::kChunks : 1;
+        // One wait for both blocks' TMEM loads of a chunk.  Of a single block
+        // the second half is another pair's stale partial: not added.
 #pragma unroll
-        for (int q0 = 0; q0 < C::kChunks; q0 += kBatch) {
-          if (chunk0(q0) >= n) break;
-          uint32_t d[kBatch][C::kTiles][16];
+        for (int q = 0; q < C::kChunks; ++q) {
+          if (chunk0(q) >= n) break;
 #pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            if (chunk0(q0 + q) >= n) break;
+          for (int t = 0; t < C::kTiles; ++t) {
+            uint32_t d[2][16];
 #pragma unroll
-            for (int t = 0; t < C::kTiles; ++t)
-              tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(b * C::kBufCols + t * NT + chunk0(q0 + q)), d[q][t]);
-          }
-          tmem_wait_ld();
+            for (int h = 0; h < 2; ++h)
+              tmem_ld_32x32b_x16(lane_base + static_cast<uint32_t>(b * C::kBufCols + h * C::kBlockCols + t * NT + chunk0(q)),
+                                 d[h]);
+            tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            if (chunk0(q0 + q) >= n) break;
-#pragma unroll
-            for (int t = 0; t < C::kTiles; ++t)
+            for (int h = 0; h < 2; ++h) {
+              if (h == blocks) break;
+              const float4* sc = reinterpret_cast<const float4*>(sSc + (h == 0 ? s0 : s1) * C::kTiles * NT + t * NT + chunk0(q));
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float4 f = sc[(t * NT + chunk0(q0 + q)) / 4 + i];
-                float* a = &acc[q0 + q][t][4 * i];
-                const uint32_t* x = &d[q][t][4 * i];
-                a[0] = __fmaf_rn(__uint_as_float(x[0]), f.x, a[0]);
-                a[1] = __fmaf_rn(__uint_as_float(x[1]), f.y, a[1]);
-                a[2] = __fmaf_rn(__uint_as_float(x[2]), f.z, a[2]);
-                a[3] = __fmaf_rn(__uint_as_float(x[3]), f.w, a[3]);
+                const float4 f = sc[i];
+                float* a = &acc[q][t][4 * i];
+                const uint32_t* v = &d[h][4 * i];
+                a[0] = __fmaf_rn(__uint_as_float(v[0]), f.x, a[0]);
+                a[1] = __fmaf_rn(__uint_as_float(v[1]), f.y, a[1]);
+                a[2] = __fmaf_rn(__uint_as_float(v[2]), f.z, a[2]);
+                a[3] = __fmaf_rn(__uint_as_float(v[3]), f.w, a[3]);
               }
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&tempty[b]);
-          mbar_arrive(&empty[s]);
-        }
+        if (lane == 0) mbar_arrive(&tempty[b]);
+        it += blocks;
       }
       if (!ok) break;
 
       if constexpr (MODE == kFewDown) {
-        // the expert's tokens, weighted, into the block's fp32 sums.  The
-        // groups hold different tokens of one expert, but a token may change
-        // groups from one expert to the next: each expert waits for the last.
+        // the expert's tokens, weighted, into the block's fp32 sums, eight in
+        // flight.  The groups hold different tokens of one expert, but a token
+        // may change groups from one expert to the next: each expert waits
+        // for the last.
         if (C::kGroups > 1 && segs > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(seg_bar, (segs - 1) & 1u))) {
           expired();
           break;
         }
 #pragma unroll
         for (int q = 0; q < C::kChunks; ++q) {
-          if (chunk0(q) >= n) break;
-          const int at = pair0 + chunk0(q) + lane;
-          const bool in = lane < 16 && chunk0(q) + lane < n;
-          const int tok = in ? sTok[at] : 0;
-          const float wt = in ? sWt[at] : 0.0f;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (chunk0(q) + i >= n) break;
-            float* to = sAcc + __shfl_sync(0xFFFFFFFFu, tok, i) * 128 + row;
-            *to = __fmaf_rn(__shfl_sync(0xFFFFFFFFu, wt, i), acc[q][0][i], *to);
+          for (int h = 0; h < 2; ++h) {
+            const int t0 = chunk0(q) + h * 8;
+            if (t0 >= n) break;
+            float* to[8];
+            float w[8], old[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int at = pair0 + (t0 + i < n ? t0 + i : t0);
+              to[i] = sAcc + sTok[at] * 128 + row;
+              w[i] = sWt[at];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) old[i] = *to[i];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (t0 + i < n) *to[i] = __fmaf_rn(w[i], acc[q][0][h * 8 + i], old[i]);
           }
         }
         if (C::kGroups > 1) {
@@ -833,30 +872,34 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
         // small: it runs once per 128 columns, from a cold instruction cache
 #pragma unroll 1
         for (int c = 0; c < kSubs && sub0(c) < n; ++c) {
+          float x[C::kTiles][C::kRedTok];
 #pragma unroll
           for (int cc = 0; cc < kSubs; ++cc)
-            if (cc == c)
-              meet_put(n - sub0(c), [&](int q, int t) {
-                const int i = cc * C::kRedTok + q;
-                return acc[i / 16][t][i % 16];
-              });
+            if (cc == c) {
+#pragma unroll
+              for (int t = 0; t < C::kTiles; ++t)
+#pragma unroll
+                for (int q = 0; q < C::kRedTok; ++q) x[t][q] = acc[(cc * C::kRedTok + q) / 16][t][(cc * C::kRedTok + q) % 16];
+            }
+          if (S > 1) meet(x, n - sub0(c));
           if (!ok) break;
           if constexpr (MODE == kFewLinear) {
             if (c > 0) load_res(c);
-            finish_rows(c, [&](int slot) { return sum_of(slot, 0); });
+            finish_rows(c, x[0]);
           } else {
             // h = silu(g) u in fp32, its 1x128 group (the 128 threads' rows)
-            // quantized straight from fp32: no rounding to bf16 on the way
-            const int own = (n - sub0(c) < C::kRedTok ? n - sub0(c) : C::kRedTok);   // tokens of this meeting
-            if (rank < own) {
+            // quantized straight from fp32: no rounding to bf16 on the way.
+            // Slots without a token are computed along and not stored.
+            const int own = own_of(c, n);
+            if (own > 0) {
               float* am = sAmax + (grp * 2 + (quants & 1u)) * 4 * C::kRedTok;
-#pragma unroll 1
-              for (int q = rank, slot = 0; q < own; q += S, ++slot) {
-                const float g = sum_of(slot, 0), u = sum_of(slot, 1);
-                const float h = __fdiv_rn(g, 1.0f + expf(-g)) * u;
-                red[slot * C::kTiles * 128 + row] = h;       // read back by this thread alone
-                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
-                if (lane == 0) am[slot * 4 + quad] = __uint_as_float(top);
+              float h[C::kRedTok];
+#pragma unroll
+              for (int k = 0; k < C::kRedTok; ++k) h[k] = __fdiv_rn(x[0][k], 1.0f + expf(-x[0][k])) * x[1][k];
+#pragma unroll
+              for (int k = 0; k < C::kRedTok; ++k) {
+                const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h[k]) & 0x7FFFFFFFu);
+                if (lane == 0) am[k * 4 + quad] = __uint_as_float(top);
               }
               __syncwarp();
               if (lane == 0) mbar_arrive(&amax_bar[grp]);
@@ -865,20 +908,22 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
                 break;
               }
               ++quants;
-#pragma unroll 1
-              for (int q = rank, slot = 0; q < own; q += S, ++slot) {
+              const uint64_t r0 = static_cast<uint64_t>(pair0 + sub0(c) + rank);
+              FGFP8_DCHECK(r0 + ((own - 1) << lgS) < static_cast<uint64_t>(p.T) * p.topk && sg.j * 128 + row < p.I);
+#pragma unroll
+              for (int k = 0; k < C::kRedTok; ++k) {
                 // magnitude bits compare like the values, and a NaN above all of them
-                const uint32_t* m4 = reinterpret_cast<const uint32_t*>(am) + slot * 4;
-                const float scale = scale_of_f32(__uint_as_float(max(max(m4[0], m4[1]), max(m4[2], m4[3]))), p.fmt);
-                const uint64_t r = static_cast<uint64_t>(pair0 + sub0(c) + q);
-                FGFP8_DCHECK(r < static_cast<uint64_t>(p.T) * p.topk && sg.j * 128 + row < p.I);
-                p.Hq[r * p.I + sg.j * 128 + row] = __nv_cvt_float_to_fp8(
-                    __fdiv_rn(red[slot * C::kTiles * 128 + row], scale), __NV_SATFINITE, __NV_E4M3);
-                if (row == 0) p.Hs[r * (p.I / 128) + sg.j] = scale;
+                const uint4 m4 = *reinterpret_cast<const uint4*>(am + k * 4);
+                const float scale = scale_of_f32(__uint_as_float(max(max(m4.x, m4.y), max(m4.z, m4.w))), p.fmt);
+                const uint8_t code = __nv_cvt_float_to_fp8(__fdiv_rn(h[k], scale), __NV_SATFINITE, __NV_E4M3);
+                const uint64_t r = r0 + (static_cast<uint64_t>(k) << lgS);
+                if (k < own) {
+                  p.Hq[r * p.I + sg.j * 128 + row] = code;
+                  if (row == 0) p.Hs[r * (p.I / 128) + sg.j] = scale;
+                }
               }
             }
           }
-          meet_done();
         }
         if (!ok) break;
       }
@@ -890,14 +935,16 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       if (C::kGroups > 1 && ok && segs > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(seg_bar, (segs - 1) & 1u))) expired();
 #pragma unroll 1
       for (int c = 0; c < kSubs && sub0(c) < p.T && ok; ++c) {
-        const float* from = sAcc + sub0(c) * 128 + row;
-        if (S > 1) meet_put(p.T - sub0(c), [&](int q, int) { return from[q * 128]; });
+        float x[1][C::kRedTok];
+#pragma unroll
+        for (int q = 0; q < C::kRedTok; ++q) x[0][q] = sAcc[(sub0(c) + q) * 128 + row];
+        if (S > 1) meet(x, p.T - sub0(c));
         if (!ok) break;
         if (c > 0) load_res(c);
-        finish_rows(c, [&](int slot) { return S > 1 ? sum_of(slot, 0) : from[slot * 128]; });
-        meet_done();
+        finish_rows(c, x[0]);
       }
     }
+    if (S > 1 && meets == 0) cluster_wait();
   }
 
   // ---- teardown
@@ -905,7 +952,11 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (S > 1) cluster_sync();                      // no rank leaves while another may still write to it
+  if (S > 1) {                                    // no rank leaves while another may still write to it
+    if (warp >= kTokWarp0) cluster_wait();        // (the first phase)
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == kMmaWarp) tmem_dealloc(tmem_base, C::kTmemCols);
 }
 
