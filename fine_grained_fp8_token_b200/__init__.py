@@ -53,7 +53,7 @@ SIGNATURES = {
                                      _I64, _P]),
     "fgfp8_route_topk": (_INT, [_P, _INT, _I64, _P, _I64, _I64, _I64, _INT, _I64, _I64, _INT, ctypes.c_float, _P, _P,
                                 _P]),
-    "fgfp8_moe_workspace_bytes": (_INT, [_I64, _I64, _I64, ctypes.POINTER(_I64)]),
+    "fgfp8_moe_workspace_bytes": (_INT, [_I64, _I64, _I64, _I64, ctypes.POINTER(_I64)]),
     "fgfp8_moe_decode": (_INT, [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
                                 _INT, _P]),
     "fgfp8_check_device_status": (_INT, [_P]),
@@ -595,10 +595,10 @@ def route_topk(logits, topk: int, score: str = "softmax", bias=None, n_group: in
     return _run_on(dev, stream, where, call)
 
 
-def moe_workspace_bytes(T: int, topk: int, I: int) -> int:
+def moe_workspace_bytes(T: int, topk: int, K: int, I: int) -> int:
     """Bytes of moe_decode's workspace."""
     n = ctypes.c_int64()
-    _check(fgfp8_moe_workspace_bytes(T, topk, I, ctypes.byref(n)), "fgfp8_moe_workspace_bytes")
+    _check(fgfp8_moe_workspace_bytes(T, topk, K, I, ctypes.byref(n)), "fgfp8_moe_workspace_bytes")
     return n.value
 
 
@@ -608,7 +608,7 @@ def moe_decode(X, ids, weights, W13q, W13s, W2q, W2s, fmt: int, residual=None, Y
     [T, topk] as from route_topk, W13q [E, 2I, K] / W13s with gate and up
     interleaved (interleave_gate_up per expert), W2q [E, K, I] / W2s.
     Y[t] = bf16(residual[t] + sum_j weights[t, j] expert_{ids[t, j]}(X[t])).
-    workspace: uint8 tensor of moe_workspace_bytes(T, topk, I) (allocated here
+    workspace: uint8 tensor of moe_workspace_bytes(T, topk, K, I) (allocated here
     when not given; calls that may overlap need their own).  Returns Y."""
     where, t = "moe_decode", _torch()
     dev = X.get_device()
@@ -631,7 +631,7 @@ def moe_decode(X, ids, weights, W13q, W13s, W2q, W2s, fmt: int, residual=None, Y
         rp = residual.data_ptr()
     if Y is not None:
         _dense(Y, where, "Y", (t.bfloat16,), (T, K), dev)
-    need = moe_workspace_bytes(T, topk, I)
+    need = moe_workspace_bytes(T, topk, K, I)
     if workspace is not None:
         _dense(workspace, where, "workspace", (t.uint8,), (workspace.numel(),), dev)
     lib = load()

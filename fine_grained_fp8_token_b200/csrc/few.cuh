@@ -15,7 +15,8 @@
 //               accumulators, then the epilogue;
 //   tokens      (4 warps) each K block belongs to one of them in turn: from bf16 rows it gathers the
 //               expert's token rows, quantizes them and writes the 128-byte-
-//               swizzled tile; in both cases it writes the products sa * sw.
+//               swizzled tile; it requests rows of codes from the TMA; in both
+//               cases it writes the products sa * sw.
 //               The rows are L2-resident, and quantizing them again per weight
 //               block costs a few instructions per 16 KB of weights, which
 //               saves a quantizer kernel and the gather of rows.  One warp per
@@ -26,7 +27,7 @@
 //   TMA         (1 warp) the weight tiles and, where the source is codes, the
 //               token rows (a linear layer's rows are contiguous, and an
 //               expert's rows of H are);
-//   MMA         (1 warp) owns TMEM, issues the MMAs.
+//   MMA         (1 or 2 warps) owns TMEM, issues the MMAs.
 //
 // Few rows leave fewer 128-row weight blocks than SMs, so K is split over the
 // CTAs of a cluster.  Their partial sums meet in distributed shared memory:
@@ -121,11 +122,9 @@ struct FewCfg {
   static constexpr int kStagesFit = static_cast<int>((kBudget - kFixed) / kStageBytes);
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
   static constexpr size_t kSmemBytes = 1024 + kFixed + static_cast<size_t>(kStages) * kStageBytes;
-  // Warps that prepare token operands, K block u by warp u % kTokWarps.  At
-  // most kStages: a warp that has passed its wait for block u - kTokWarps
-  // knows that block u - kTokWarps - kStages is consumed, and its parity
-  // wait for block u tells phases apart only if that covers u - 2 kStages.
-  static constexpr int kTokWarps = kStages < 4 ? kStages : 4;
+  // Warps that prepare token operands: stage s belongs to warp s % kTokWarps,
+  // so that a warp meets every phase of its stages' barriers in turn.
+  static constexpr int kTokWarps = 4;
   // TMEM holds two pairs of K blocks: the promotion takes a pair at a time
   // (one wait for the MMAs and one for the TMEM loads of both; with single
   // blocks its chain of waits took 500 cycles a block, where 16 KB of weights
@@ -134,12 +133,16 @@ struct FewCfg {
   static constexpr uint32_t kBlockCols = kTiles * NT;
   static constexpr uint32_t kBufCols = 2 * kBlockCols;
   static constexpr uint32_t kTmemCols = kNumBuf * kBufCols;                          // 64 to 512
-  static constexpr int kThreads = (kEpiWarps + 6) * 32;
+  // Issuing a block's MMAs, commits and waits takes one warp about 480
+  // cycles.  Alone on its SM a CTA wants a block every 540 to 700, so two
+  // warps take the pairs in turn.
+  static constexpr int kMmaWarps = NT == 64 ? 2 : 1;
+  static constexpr int kThreads = (kEpiWarps + 5 + kMmaWarps) * 32;
   static_assert(kStages >= 3, "pipeline depth");
   static_assert(kScSlots >= kStages + 4, "ring of the scales");
-  static_assert(kTokWarps <= kStages && kTokWarps <= 4, "parity waits of the token warps");
+  static_assert(kMmaWarps == 1 || kStages >= 4, "parity waits of the MMA warps");
   static_assert(kTmemCols >= 32 && (kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols * kCtas <= 512, "TMEM columns");
-  static_assert((2 * kStages + kScSlots + 2 * kNumBuf + 8) * 8 + 16 <= kBarrierBytes, "barrier area");
+  static_assert((2 * kStages + kScSlots + 2 * kNumBuf + 9) * 8 + 16 <= kBarrierBytes, "barrier area");
 };
 
 // ------------------------------------------------------------ cluster helpers
@@ -195,14 +198,27 @@ __device__ __forceinline__ uint32_t load_scale_word(const void* p, uint64_t i, i
   return fmt == 0 ? __ldg(reinterpret_cast<const uint32_t*>(p) + i) : __ldg(reinterpret_cast<const uint8_t*>(p) + i);
 }
 
-// Scale of a group whose amax is a full fp32 number: max(amax, 1e-4) / 448
-// (IEEE division), or the smallest power of two not below that.
-__device__ __forceinline__ float scale_of_f32(float amax, int fmt) {
-  const float s = __fdiv_rn(amax < 1e-4f ? 1e-4f : amax, 448.0f);
-  if (fmt == 0) return s;
-  uint32_t b = __float_as_uint(s), e = b >> 23;
-  if ((b & 0x7FFFFFu) != 0u && e < 255u) e += 1u;
-  return scale_value(e, 1);
+// Scale s of a group whose amax is a full fp32 number, and r = RN(1/s):
+// max(amax, 1e-4) / 448, or the smallest power of two not below that.  The
+// quotients are Markstein's FMA form, as in make_scale and quant4; the
+// division routine's slow path (values of slots without a token, say) took
+// most of the epilogue's time.
+__device__ __forceinline__ float scale_of_f32(float amax, int fmt, float& r) {
+  const float a = amax < 1e-4f ? 1e-4f : amax;
+  constexpr float kR448 = 1.0f / 448.0f;
+  const float q0 = __fmul_rn(a, kR448);
+  float s = __fmaf_rn(__fmaf_rn(-q0, 448.0f, a), kR448, q0);
+  if (fmt != 0) {
+    uint32_t b = __float_as_uint(s), e = b >> 23;
+    if ((b & 0x7FFFFFu) != 0u && e < 255u) e += 1u;
+    s = scale_value(e, 1);
+  }
+  r = __frcp_rn(s);
+  return s;
+}
+__device__ __forceinline__ uint8_t quant_f32(float x, float s, float r) {
+  const float q0 = __fmul_rn(x, r);
+  return __nv_cvt_float_to_fp8(__fmaf_rn(__fmaf_rn(-q0, s, x), r, q0), __NV_SATFINITE, __NV_E4M3);
 }
 
 // ------------------------------------------------------------ work of a CTA
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + C::kNumBuf;
   uint64_t* mma_done = tempty + C::kNumBuf;
-  uint64_t* red_full = mma_done + 1;
+  uint64_t* red_full = mma_done + 2;
   uint64_t* red_empty = red_full + 2;
   uint64_t* amax_bar = red_empty + 2;
   uint64_t* seg_bar = amax_bar + 2;
@@ -327,7 +343,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], C::kEpiWarps);
     }
-    mbar_init(mma_done, 1);
+    for (int w = 0; w < 2; ++w) mbar_init(&mma_done[w], 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&red_full[g], 4 * S);
       mbar_init(&red_empty[g], 4 * S);
@@ -452,9 +468,13 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       for (uint32_t i = (it > static_cast<uint32_t>(C::kStages) ? it - C::kStages : 0); i < it; ++i)
         if (!mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1u)) record_status(kDevTimeoutProducer);
     }
-  } else if (warp == kMmaWarp) {
-    // ================= MMA issuer: the whole warp keeps the loop's state
-    // uniform, one elected lane issues
+  } else if (warp >= kMmaWarp) {
+    // ================= MMA issuers, a pair of K blocks each in turn: the whole
+    // warp keeps the loop's state uniform, one elected lane issues.  The wait
+    // for the pair's TMEM buffer also tells that every block before the other
+    // warp's current pair has been full, so that the parity of `full` is not
+    // mistaken for the one before the last.
+    const uint32_t me = static_cast<uint32_t>(warp - kMmaWarp);
     const uint64_t a_desc0 = smem_desc_k_sw128(smem_u32(sA)), b_desc0 = smem_desc_k_sw128(smem_u32(sB));
     uint32_t it = 0, pairs = 0;
     bool ok = true;
@@ -464,6 +484,10 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       for (int kb = sg.kb0; kb < sg.kb1 && ok; kb += 2, ++pairs) {
         const int b = pairs % C::kNumBuf;
         const int blocks = sg.kb1 - kb < 2 ? 1 : 2;
+        if (C::kMmaWarps > 1 && (pairs & 1u) != me) {
+          it += blocks;
+          continue;
+        }
         bool got = pairs < static_cast<uint32_t>(C::kNumBuf) || mbar_wait(&tempty[b], ((pairs / C::kNumBuf) & 1u) ^ 1u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -493,14 +517,19 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
         }
       }
     }
-    if (elect_one()) mma_commit(mma_done);
+    if (elect_one()) mma_commit(&mma_done[me]);
     __syncwarp();
-    if (!mbar_wait(mma_done, 0) && lane == 0) record_status(kDevTimeoutMma);
+    if (!mbar_wait(&mma_done[me], 0) && lane == 0) record_status(kDevTimeoutMma);
   } else if (warp >= kTokWarp0) {
     // ================= token operand and scales of this warp's K blocks
     uint32_t it = 0;                                                 // blocks before the segment
-    uint32_t mine = static_cast<uint32_t>(warp - kTokWarp0);         // this warp's next block
-    bool ok = warp - kTokWarp0 < C::kTokWarps;
+    const uint32_t me = static_cast<uint32_t>(warp - kTokWarp0);
+    auto mine_from = [&](uint32_t u) {                               // this warp's first block from u on
+      while ((u % C::kStages) % C::kTokWarps != me) ++u;
+      return u;
+    };
+    bool ok = me < static_cast<uint32_t>(C::kStages);                // with few stages a warp may have none
+    uint32_t mine = ok ? mine_from(0) : 0;
     while (ok && work.next(sg)) {
       const uint32_t it_end = it + static_cast<uint32_t>(sg.kb1 - sg.kb0);
       const int n = count_of(sg), pair0 = pair0_of(sg);
@@ -523,17 +552,16 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
 
       if constexpr (kBf16) {
         // lane: team lane / 8 of four, one token per team and pass, 16 of the
-        // token's 128 elements.  Chunks of 16 tokens: four passes together,
-        // so that their loads and reductions overlap, or one for up to four
-        // tokens.
+        // token's 128 elements.  Four passes together, so that their loads and
+        // reductions overlap, or one for up to four tokens.
         const int team = lane >> 3, l8 = lane & 7;
-        constexpr int kAhead = NT > 16 ? 2 : 1;                      // chunks in registers
-        uint4 v[kAhead][4][2];
-        auto load = [&](auto passes, uint4 (&v)[4][2], int c, int kb) {
+        static_assert(NT == 16, "wider tiles take codes");
+        uint4 v[4][2];
+        auto load = [&](auto passes, int kb) {
           constexpr int P = decltype(passes)::value;
 #pragma unroll
           for (int q = 0; q < P; ++q) {
-            const int i = c * 16 + q * 4 + team;
+            const int i = q * 4 + team;
             v[q][0] = v[q][1] = make_uint4(0, 0, 0, 0);
             if (i < n) {
               const int t = kMoe ? sTok[pair0 + i] : i;
@@ -544,7 +572,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             }
           }
         };
-        auto store = [&](auto passes, auto fmt, const uint4 (&v)[4][2], int c, int s, float* sc) {
+        auto store = [&](auto passes, auto fmt, int s, float* sc) {
           constexpr int P = decltype(passes)::value, F = decltype(fmt)::value;
           uint8_t* tile = sB + s * C::kBBytes;
           uint32_t am[P];
@@ -556,7 +584,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             for (int q = 0; q < P; ++q) am[q] = max(am[q], __shfl_xor_sync(0xFFFFFFFFu, am[q], o));
 #pragma unroll
           for (int q = 0; q < P; ++q) {
-            const int i = c * 16 + q * 4 + team;
+            const int i = q * 4 + team;
             const GroupScale g = make_scale<F>(am[q]);
             uint4 codes;
             codes.x = quant4<F>(v[q][0].x, v[q][0].y, g);
@@ -576,56 +604,53 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
         };
         using One = std::integral_constant<int, 1>;
         using Four = std::integral_constant<int, 4>;
-        auto load16 = [&](uint4 (&v)[4][2], int c, int kb) {
-          if (n - c * 16 > 4) load(Four{}, v, c, kb);
-          else load(One{}, v, c, kb);
-        };
-        auto store16 = [&](const uint4 (&v)[4][2], int c, int s, float* sc) {
-          using F32 = std::integral_constant<int, 0>;
-          using E8 = std::integral_constant<int, 1>;
-          if (n - c * 16 > 4) {
-            if (p.fmt == 0) store(Four{}, F32{}, v, c, s, sc);
-            else store(Four{}, E8{}, v, c, s, sc);
-          } else {
-            if (p.fmt == 0) store(One{}, F32{}, v, c, s, sc);
-            else store(One{}, E8{}, v, c, s, sc);
-          }
-        };
-        auto load_first = [&](int kb) {
-          load16(v[0], 0, kb);
-          if (kAhead > 1 && n > 16) load16(v[kAhead - 1], 1, kb);
+        using F32 = std::integral_constant<int, 0>;
+        using E8 = std::integral_constant<int, 1>;
+        auto load_all = [&](int kb) {
+          if (n > 4) load(Four{}, kb);
+          else load(One{}, kb);
           load_sw(kb);
         };
-        if (mine < it_end) load_first(kb_of(mine));
-        for (; mine < it_end; mine += C::kTokWarps) {
+        auto store_all = [&](int s, float* sc) {
+          if (n > 4) {
+            if (p.fmt == 0) store(Four{}, F32{}, s, sc);
+            else store(Four{}, E8{}, s, sc);
+          } else {
+            if (p.fmt == 0) store(One{}, F32{}, s, sc);
+            else store(One{}, E8{}, s, sc);
+          }
+        };
+        if (mine < it_end) load_all(kb_of(mine));
+        while (mine < it_end) {
           const int kb = kb_of(mine);
+          const uint32_t next = mine_from(mine + 1);
           const int s = mine % C::kStages;
           if (!stage_free(mine)) {
             ok = false;
             break;
           }
           float* sc = sSc + (mine % C::kScSlots) * C::kTiles * NT;
-          store16(v[0], 0, s, sc);
-          if constexpr (kAhead > 1) {
-            if (n > 32) load16(v[0], 2, kb);
-            if (n > 16) store16(v[1], 1, s, sc);
-            if (n > 48) load16(v[1], 3, kb);
-            if (n > 32) store16(v[0], 2, s, sc);
-            if (n > 48) store16(v[1], 3, s, sc);
-          }
+          store_all(s, sc);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&full[s]);
             mbar_arrive(&sc_full[mine % C::kScSlots]);
           }
-          if (mine + C::kTokWarps < it_end) load_first(kb + C::kTokWarps);
+          if (next < it_end) load_all(kb_of(next));
+          mine = next;
         }
       } else {
-        // lane: the scales of tokens lane, lane + 32; lane 0 requests the rows
+        // lane: the scales of tokens lane, lane + 32.  Lane 0 requests the rows
+        // where they are contiguous, 16 at a time; GateUp's are anyone's rows
+        // of X, and each lane requests its own.
         constexpr int kTok = (NT + 31) / 32;
         const int n16 = (n + 15) >> 4;
         uint32_t sa[kTok];
+        int tok[kTok];
+#pragma unroll
+        for (int q = 0; q < kTok; ++q)
+          tok[q] = MODE == kFewGateUp && q * 32 + lane < n ? sTok[pair0 + q * 32 + lane] : q * 32 + lane;
         auto load_sa = [&](int kb) {
 #pragma unroll
           for (int q = 0; q < kTok; ++q) {
@@ -635,7 +660,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
               if (MODE == kFewDown)                                  // written by GateUp: a plain load
                 sa[q] = reinterpret_cast<const uint32_t*>(p.src_scale)[static_cast<uint64_t>(pair0 + i) * p.KB + kb];
               else
-                sa[q] = load_scale_word(p.src_scale, i + static_cast<uint64_t>(kb) * p.ld_s, p.fmt);
+                sa[q] = load_scale_word(p.src_scale, tok[q] + static_cast<uint64_t>(kb) * p.ld_s, p.fmt);
             }
           }
         };
@@ -643,31 +668,45 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           load_sa(kb_of(mine));
           load_sw(kb_of(mine));
         }
-        for (; mine < it_end; mine += C::kTokWarps) {
+        while (mine < it_end) {
           const int kb = kb_of(mine);
+          const uint32_t next = mine_from(mine + 1);
           const int s = mine % C::kStages;
           if (!stage_free(mine)) {
             ok = false;
             break;
           }
           float* sc = sSc + (mine % C::kScSlots) * C::kTiles * NT;
-          const float w = scale_value(sw[0], p.fmt);
+          uint8_t* tile = sB + s * C::kBBytes;
 #pragma unroll
           for (int q = 0; q < kTok; ++q) {
             const int i = q * 32 + lane;
-            if (i < n) sc[i] = w * (MODE == kFewDown ? __uint_as_float(sa[q]) : scale_value(sa[q], p.fmt));
+            const float a = MODE == kFewDown ? __uint_as_float(sa[q]) : scale_value(sa[q], p.fmt);
+            if (i < n) {
+#pragma unroll
+              for (int t = 0; t < C::kTiles; ++t) sc[t * NT + i] = a * scale_value(sw[t], p.fmt);
+            }
           }
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sc_full[mine % C::kScSlots]);
-            mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n16 * 2048));
-            for (int c = 0; c < n16; ++c)
-              tma_load_2d(sB + s * C::kBBytes + c * 2048, &tmX, &full[s], kb * 128, pair0 + c * 16);
+          if (MODE == kFewGateUp) {
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n * 128));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sc_full[mine % C::kScSlots]);
+#pragma unroll
+            for (int q = 0; q < kTok; ++q)
+              if (q * 32 + lane < n) tma_load_2d(tile + (q * 32 + lane) * 128, &tmX, &full[s], kb * 128, tok[q]);
+          } else {
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sc_full[mine % C::kScSlots]);
+              mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n16 * 2048));
+              for (int c = 0; c < n16; ++c) tma_load_2d(tile + c * 2048, &tmX, &full[s], kb * 128, pair0 + c * 16);
+            }
           }
-          if (mine + C::kTokWarps < it_end) {
-            load_sa(kb + C::kTokWarps);
-            load_sw(kb + C::kTokWarps);
+          if (next < it_end) {
+            load_sa(kb_of(next));
+            load_sw(kb_of(next));
           }
+          mine = next;
         }
       }
       it = it_end;
@@ -895,7 +934,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
               float* am = sAmax + (grp * 2 + (quants & 1u)) * 4 * C::kRedTok;
               float h[C::kRedTok];
 #pragma unroll
-              for (int k = 0; k < C::kRedTok; ++k) h[k] = __fdiv_rn(x[0][k], 1.0f + expf(-x[0][k])) * x[1][k];
+              for (int k = 0; k < C::kRedTok; ++k) h[k] = times_sigmoid(x[0][k], x[0][k]) * x[1][k];
 #pragma unroll
               for (int k = 0; k < C::kRedTok; ++k) {
                 const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h[k]) & 0x7FFFFFFFu);
@@ -914,8 +953,9 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
               for (int k = 0; k < C::kRedTok; ++k) {
                 // magnitude bits compare like the values, and a NaN above all of them
                 const uint4 m4 = *reinterpret_cast<const uint4*>(am + k * 4);
-                const float scale = scale_of_f32(__uint_as_float(max(max(m4.x, m4.y), max(m4.z, m4.w))), p.fmt);
-                const uint8_t code = __nv_cvt_float_to_fp8(__fdiv_rn(h[k], scale), __NV_SATFINITE, __NV_E4M3);
+                float inv;
+                const float scale = scale_of_f32(__uint_as_float(max(max(m4.x, m4.y), max(m4.z, m4.w))), p.fmt, inv);
+                const uint8_t code = quant_f32(h[k], scale, inv);
                 const uint64_t r = r0 + (static_cast<uint64_t>(k) << lgS);
                 if (k < own) {
                   p.Hq[r * p.I + sg.j * 128 + row] = code;

@@ -711,7 +711,8 @@ fgfp8_status launch_few(const uint8_t* W, uint64_t rows, uint64_t src_rows, fgfp
   fgfp8_status st = make_map_u8_sw128(&mW, W, rows, K, K, 128 * C::kTiles, dev);
   if (st != FGFP8_OK) return st;
   if (!kBf16) {
-    st = make_map_u8_sw128(&mX, a.src, src_rows, K, K, 16, dev);      // token codes, 16 rows per copy
+    // token codes: 16 rows per copy, or single ones where they are gathered
+    st = make_map_u8_sw128(&mX, a.src, src_rows, K, K, MODE == fgfp8::kFewGateUp ? 1 : 16, dev);
     if (st != FGFP8_OK) return st;
   }
   auto kernel = fgfp8::few_kernel<MODE, NT, kBf16>;
@@ -772,10 +773,10 @@ fgfp8_status few_linear(const void* src, int64_t ld_src, const void* Xs, int64_t
   a.epi = epi;
   a.early = early;
   const char* what = "few-token linear launch";
-  if (M <= 16)
+  if (kBf16 || M <= 16)
     return launch_few<fgfp8::kFewLinear, 16, kBf16>(Wq, static_cast<uint64_t>(N), static_cast<uint64_t>(M), a, a.NB, stream,
                                                       dev, sm_count, what);
-  return launch_few<fgfp8::kFewLinear, 64, kBf16>(Wq, static_cast<uint64_t>(N), static_cast<uint64_t>(M), a, a.NB, stream,
+  return launch_few<fgfp8::kFewLinear, 64, false>(Wq, static_cast<uint64_t>(N), static_cast<uint64_t>(M), a, a.NB, stream,
                                                       dev, sm_count, what);
 }
 
@@ -810,14 +811,26 @@ fgfp8_status gemm_epilogue_impl(const uint8_t* Xq, const void* Xs, int64_t ld_s,
                                                                     dev, sms, early, 0, nullptr, nullptr, 0, -1, epi);
 }
 
-// Workspace of fgfp8_moe_decode: the codes of H [T * topk, I], then its scales.
-int64_t moe_codes_bytes(int64_t T, int64_t topk, int64_t I) { return (T * topk * I + 255) / 256 * 256; }
-int64_t moe_workspace_need(int64_t T, int64_t topk, int64_t I) {
-  return moe_codes_bytes(T, topk, I) + T * topk * (I / 128) * 4;
-}
+// Workspace of fgfp8_moe_decode: codes of H [T * topk, I] and its scales, and
+// for more than FGFP8_FUSED_QUANT_TOKENS tokens the codes and scales of X.
+struct MoeWorkspace {
+  int64_t hs, xq, xs, bytes;         // offsets, and the whole size
+  int64_t ld_s;
+  MoeWorkspace(int64_t T, int64_t topk, int64_t K, int64_t I) {
+    auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
+    hs = up(T * topk * I);
+    xq = up(hs + T * topk * (I / 128) * 4);
+    ld_s = (T + 15) / 16 * 16;
+    const bool quant = T > FGFP8_FUSED_QUANT_TOKENS;
+    xs = quant ? up(xq + T * K) : xq;
+    bytes = quant ? xs + ld_s * (K / 128) * 4 : xq;
+  }
+};
 
-fgfp8_status check_moe_sizes(int64_t T, int64_t topk, int64_t I) {
-  if (T < 0 || topk < 0 || I < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
+fgfp8_status check_moe_sizes(int64_t T, int64_t topk, int64_t K, int64_t I) {
+  if (T < 0 || topk < 0 || K < 0 || I < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
+  if (K == 0 || K % 128 != 0) return fail(FGFP8_ERR_SHAPE, "K must be a positive multiple of 128");
+  if (K > (int64_t(1) << 20)) return fail(FGFP8_ERR_SHAPE, "K must be <= 2^20");
   if (T > fgfp8::kFewMaxTokens) return fail(FGFP8_ERR_SHAPE, "T must be <= FGFP8_MOE_MAX_TOKENS (64)");
   if (topk < 1 || topk > fgfp8::kFewMaxTopk) return fail(FGFP8_ERR_SHAPE, "topk must be in [1, 16]");
   if (I == 0 || I % 128 != 0) return fail(FGFP8_ERR_SHAPE, "I must be a positive multiple of 128");
@@ -825,7 +838,7 @@ fgfp8_status check_moe_sizes(int64_t T, int64_t topk, int64_t I) {
   return FGFP8_OK;
 }
 
-template <int NT>
+template <int NT, bool kBf16>
 fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const float* weights, const uint8_t* W13q,
                         const void* W13s, const uint8_t* W2q, const void* W2s, const fgfp8::EpiArgs& epi, void* Y,
                         uint8_t* ws, int64_t T, int64_t topk, int64_t E, int64_t K, int64_t I, int fmt,
@@ -838,17 +851,27 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
   a.topk = static_cast<int>(topk);
   a.E = static_cast<int>(E);
   a.Hq = ws;
-  a.Hs = reinterpret_cast<float*>(ws + moe_codes_bytes(T, topk, I));
+  const MoeWorkspace at(T, topk, K, I);
+  a.Hs = reinterpret_cast<float*>(ws + at.hs);
   a.I = static_cast<int>(I);
   const int64_t most = E < T * topk ? E : T * topk;            // experts that the tokens can meet
   // gate/up: [E, 2I, K]
   a.src = X;
   a.ld_src = static_cast<uint64_t>(ldx);
+  fgfp8_status st;
+  if (!kBf16) {
+    st = quant_act_impl(X, T, K, ldx, ws + at.xq, ws + at.xs, at.ld_s, fmt, s, false);
+    if (st != FGFP8_OK) return st;
+    a.src = ws + at.xq;
+    a.ld_src = static_cast<uint64_t>(K);
+    a.src_scale = ws + at.xs;
+    a.ld_s = static_cast<uint64_t>(at.ld_s);
+  }
   a.Ws = W13s;
   a.KB = static_cast<int>(K / 128);
   a.NB = static_cast<int>(2 * I / 128);
-  fgfp8_status st = launch_few<fgfp8::kFewGateUp, NT, true>(W13q, static_cast<uint64_t>(E) * 2 * I, 0, a, most * (I / 128),
-                                                            s, dev, sms, "expert gate/up launch");
+  st = launch_few<fgfp8::kFewGateUp, NT, kBf16>(W13q, static_cast<uint64_t>(E) * 2 * I, static_cast<uint64_t>(T), a,
+                                                most * (I / 128), s, dev, sms, "expert gate/up launch");
   if (st != FGFP8_OK) return st;
   // down: [E, K, I]
   a.src = a.Hq;
@@ -1256,11 +1279,11 @@ fgfp8_status fgfp8_route_topk(const void* logits, int logits_type, int64_t ld, c
   return logits_type == FGFP8_F32 ? launch_route<false, float>(a, s) : launch_route<false, __nv_bfloat16>(a, s);
 }
 
-fgfp8_status fgfp8_moe_workspace_bytes(int64_t T, int64_t topk, int64_t I, int64_t* bytes) {
-  fgfp8_status st = check_moe_sizes(T, topk, I);
+fgfp8_status fgfp8_moe_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t* bytes) {
+  fgfp8_status st = check_moe_sizes(T, topk, K, I);
   if (st != FGFP8_OK) return st;
   if (!bytes) return fail(FGFP8_ERR_INVALID_ARG, "bytes is NULL");
-  *bytes = moe_workspace_need(T, topk, I);
+  *bytes = MoeWorkspace(T, topk, K, I).bytes;
   return ok();
 }
 
@@ -1270,12 +1293,10 @@ fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, co
                               int64_t T, int64_t topk, int64_t E, int64_t K, int64_t I, int fmt, void* stream) {
   fgfp8_status st = check_fmt(fmt);
   if (st != FGFP8_OK) return st;
-  if (E < 0 || K < 0 || ldx < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
-  st = check_moe_sizes(T, topk, I);
+  if (E < 0 || ldx < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
+  st = check_moe_sizes(T, topk, K, I);
   if (st != FGFP8_OK) return st;
   if (E < 1 || E > fgfp8::kFewMaxExperts) return fail(FGFP8_ERR_SHAPE, "E must be in [1, 512]");
-  if (K == 0 || K % 128 != 0) return fail(FGFP8_ERR_SHAPE, "K must be a positive multiple of 128");
-  if (K > (int64_t(1) << 20)) return fail(FGFP8_ERR_SHAPE, "K must be <= 2^20");
   if (E * 2 * I >= (int64_t(1) << 31) || E * K >= (int64_t(1) << 31))
     return fail(FGFP8_ERR_SHAPE, "E*2*I and E*K must be < 2^31");
   if (ldx < K) return fail(FGFP8_ERR_SHAPE, "ldx must be >= K");
@@ -1289,7 +1310,7 @@ fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, co
   if (fmt == FGFP8_SCALE_F32 && (!aligned(W13s, 4) || !aligned(W2s, 4)))
     return fail(FGFP8_ERR_ALIGN, "fp32 W13s and W2s must be 4-byte aligned");
   if (!aligned(workspace, 256)) return fail(FGFP8_ERR_ALIGN, "workspace must be 256-byte aligned");
-  if (workspace_bytes < moe_workspace_need(T, topk, I))
+  if (workspace_bytes < MoeWorkspace(T, topk, K, I).bytes)
     return fail(FGFP8_ERR_SHAPE, "workspace_bytes is below fgfp8_moe_workspace_bytes");
   st = check_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r, K);
   if (st != FGFP8_OK) return st;
@@ -1300,10 +1321,10 @@ fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, co
   const fgfp8::EpiArgs epi = make_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (T <= 16)
-    return launch_moe<16>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
+  if (T <= FGFP8_FUSED_QUANT_TOKENS)
+    return launch_moe<16, true>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
                           info.sm_count);
-  return launch_moe<64>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
+  return launch_moe<64, false>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
                         info.sm_count);
 }
 

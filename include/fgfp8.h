@@ -294,8 +294,9 @@ fgfp8_status fgfp8_route_topk(const void* logits, int logits_type, int64_t ld, c
                               float scale, int32_t* ids, float* weights, void* stream);
 
 /*
- * A whole SwiGLU expert layer for a few tokens (decode), in two kernels; the
- * grouped and masked calls above serve larger batches.  For token t:
+ * A whole SwiGLU expert layer for a few tokens (decode), in two kernels up to
+ * FGFP8_FUSED_QUANT_TOKENS tokens and with the quantizer before them above;
+ * the grouped and masked calls above serve larger batches.  For token t:
  *   (g, u) = W13[e] x_hat          x_hat: fgfp8_quant_act of x_t
  *   h      = silu(g) * u           in fp32, quantized per 1x128 group straight
  *                                  from fp32 (amax, scale and code as in
@@ -327,7 +328,7 @@ fgfp8_status fgfp8_route_topk(const void* logits, int logits_type, int64_t ld, c
 #define FGFP8_MOE_MAX_TOKENS 64
 
 /* *bytes (host memory): the workspace of fgfp8_moe_decode at these sizes. */
-fgfp8_status fgfp8_moe_workspace_bytes(int64_t T, int64_t topk, int64_t I, int64_t* bytes);
+fgfp8_status fgfp8_moe_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t* bytes);
 
 fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, const float* weights,
                               const uint8_t* W13q, const void* W13s, const uint8_t* W2q, const void* W2s,

@@ -94,13 +94,17 @@ def test_moe_refusals(bad, code):
 
 def test_moe_workspace_size():
     n = ctypes.c_int64(-5)
-    assert fg.fgfp8_moe_workspace_bytes(3, 2, 128, ctypes.byref(n)) == OK
-    assert n.value == 768 + 6 * 4
-    assert fg.moe_workspace_bytes(0, 1, 128) == 0
-    assert fg.fgfp8_moe_workspace_bytes(65, 2, 128, ctypes.byref(n)) == SHAPE
-    assert fg.fgfp8_moe_workspace_bytes(3, 2, 100, ctypes.byref(n)) == SHAPE
-    assert fg.fgfp8_moe_workspace_bytes(3, 2, 128, None) == INVALID
-    need = fg.moe_workspace_bytes(4, 2, 128)
+    f = fg.fgfp8_moe_workspace_bytes
+    # codes of H, then its scales, each from a 256-byte boundary
+    assert f(3, 2, 256, 128, ctypes.byref(n)) == OK and n.value == 768 + 256
+    # above 16 tokens the codes of X and its scales too
+    assert f(17, 1, 256, 128, ctypes.byref(n)) == OK and n.value == 2304 + 256 + 4352 + 32 * 2 * 4
+    assert fg.moe_workspace_bytes(0, 1, 128, 128) == 0
+    assert f(65, 2, 256, 128, ctypes.byref(n)) == SHAPE
+    assert f(3, 2, 256, 100, ctypes.byref(n)) == SHAPE
+    assert f(3, 2, 100, 128, ctypes.byref(n)) == SHAPE
+    assert f(3, 2, 256, 128, None) == INVALID
+    need = fg.moe_workspace_bytes(4, 2, 256, 128)
     assert moe(ws_bytes=need - 1) == SHAPE
     assert moe(T=0, ws=None, ws_bytes=0, X=None) == OK
 

@@ -138,7 +138,7 @@ def test_against_the_formula(dev, T, E, topk, K, I, fmt):
     ids, w = route(T, E, topk, seed=T + 1)
     R = workloads.activations((T, K), "normal", seed=T + 2) if T % 2 else None
     out = Guarded((T, K), torch.bfloat16, dev)
-    n = fg.moe_workspace_bytes(T, topk, I)
+    n = fg.moe_workspace_bytes(T, topk, K, I)
     ws = Guarded((n,), torch.uint8, dev, fill=0xFF)          # NaN codes and scales: nothing stale is read
     Y = run(dev, X, ids, w, W, fmt, R, Y=out.t, workspace=ws.t)
     fg.check_device_status()
@@ -226,7 +226,7 @@ def test_graph_replays_with_other_routing(dev):
     ids = torch.full((T, topk), -1, dtype=torch.int32, device=dev)
     w = torch.zeros(T, topk, device=dev)
     Y = torch.empty(T, K, dtype=torch.bfloat16, device=dev)
-    ws = torch.empty(fg.moe_workspace_bytes(T, topk, I), dtype=torch.uint8, device=dev)
+    ws = torch.empty(fg.moe_workspace_bytes(T, topk, K, I), dtype=torch.uint8, device=dev)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         fg.moe_decode(X, ids, w, *W, fmt, Y=Y, workspace=ws)
