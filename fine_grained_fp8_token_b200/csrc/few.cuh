@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       if constexpr (MODE == kFewLinear) {
 #pragma unroll
         for (int k = 0; k < C::kRedTok; ++k) x[k] += bias;
-        apply_act8(x, p.epi.act);
+        apply_act_n(x, p.epi.act);
       }
       FGFP8_DCHECK(col < p.N && (own == 0 || sub0(c) + rank + ((own - 1) << lgS) < p.T));
       __nv_bfloat16* to = p.Y + static_cast<uint64_t>(sub0(c) + rank) * p.N + col;

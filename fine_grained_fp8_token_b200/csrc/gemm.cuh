@@ -662,6 +662,23 @@ __global__ void __launch_bounds__(GemmCfg<BN, CW>::kThreads, 1)
         }
       }
 
+      if constexpr (kEpi) {
+        // bias, activation and residual: 32 columns a pass in fp32
+        staged_epilogue<COLS / 32>(
+            [&](int p, auto at) {
+#pragma unroll
+              for (int pp = 0; pp < COLS / 32; ++pp)
+                if (pp == p) {
+#pragma unroll
+                  for (int c = 0; c < 8; ++c)
+                    *at(c) = make_float4(acc2[pp * 16 + 2 * c].x, acc2[pp * 16 + 2 * c].y, acc2[pp * 16 + 2 * c + 1].x,
+                                         acc2[pp * 16 + 2 * c + 1].y);
+                }
+            },
+            sStg + ew * C::kWarpStageBytes, lane, epi, Y, N, m0 + quad * 32, row_end, n0 + col0);
+        return;
+      }
+
       // Epilogue: bf16 (round-to-nearest-even), transposed through the warp's
       // shared-memory slot so that each store instruction writes four whole
       // 128-byte row segments.  Per 64-column pass, lane l writes its row's
@@ -670,31 +687,18 @@ __global__ void __launch_bounds__(GemmCfg<BN, CW>::kThreads, 1)
       uint8_t* slot = sStg + ew * C::kWarpStageBytes;
 #pragma unroll
       for (int p = 0; p < COLS / 64; ++p) {
-        [[maybe_unused]] uint4 res[8];              // kEpi: this row's residual of the pass, all loads in flight
-        if constexpr (kEpi) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            res[c] = live ? load_residual8(epi, m, n0 + col0 + p * 64 + c * 8) : make_uint4(0, 0, 0, 0);
-        }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const int j = p * 64 + c * 8;
           uint4 v;
-          if constexpr (kEpi) {
-            float x[8];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) x[2 * q] = acc2[j / 2 + q].x, x[2 * q + 1] = acc2[j / 2 + q].y;
-            v = epilogue8(x, epi, n0 + col0 + j, res[c]);
-          } else {
-            __nv_bfloat162 h0 = __floats2bfloat162_rn(acc2[j / 2 + 0].x, acc2[j / 2 + 0].y);
-            __nv_bfloat162 h1 = __floats2bfloat162_rn(acc2[j / 2 + 1].x, acc2[j / 2 + 1].y);
-            __nv_bfloat162 h2 = __floats2bfloat162_rn(acc2[j / 2 + 2].x, acc2[j / 2 + 2].y);
-            __nv_bfloat162 h3 = __floats2bfloat162_rn(acc2[j / 2 + 3].x, acc2[j / 2 + 3].y);
-            v.x = *reinterpret_cast<uint32_t*>(&h0);
-            v.y = *reinterpret_cast<uint32_t*>(&h1);
-            v.z = *reinterpret_cast<uint32_t*>(&h2);
-            v.w = *reinterpret_cast<uint32_t*>(&h3);
-          }
+          __nv_bfloat162 h0 = __floats2bfloat162_rn(acc2[j / 2 + 0].x, acc2[j / 2 + 0].y);
+          __nv_bfloat162 h1 = __floats2bfloat162_rn(acc2[j / 2 + 1].x, acc2[j / 2 + 1].y);
+          __nv_bfloat162 h2 = __floats2bfloat162_rn(acc2[j / 2 + 2].x, acc2[j / 2 + 2].y);
+          __nv_bfloat162 h3 = __floats2bfloat162_rn(acc2[j / 2 + 3].x, acc2[j / 2 + 3].y);
+          v.x = *reinterpret_cast<uint32_t*>(&h0);
+          v.y = *reinterpret_cast<uint32_t*>(&h1);
+          v.z = *reinterpret_cast<uint32_t*>(&h2);
+          v.w = *reinterpret_cast<uint32_t*>(&h3);
           *reinterpret_cast<uint4*>(slot + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
         }
         __syncwarp();
@@ -1129,25 +1133,20 @@ __global__ void __launch_bounds__(MxCfg<BN>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[tb]);
-      if (m < row_end) {
+      if constexpr (kEpi) {
+        if (m < row_end) row_epilogue(p, epi, Y, N, m, n0 + col0);
+      } else if (m < row_end) {
 #pragma unroll
         for (int j = 0; j < 128; j += 8) {
           uint4 v;
-          if constexpr (kEpi) {
-            float x[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = __uint_as_float(p[j + q]);
-            v = epilogue8(x, epi, n0 + col0 + j, load_residual8(epi, m, n0 + col0 + j));
-          } else {
-            __nv_bfloat162 h0 = __floats2bfloat162_rn(__uint_as_float(p[j + 0]), __uint_as_float(p[j + 1]));
-            __nv_bfloat162 h1 = __floats2bfloat162_rn(__uint_as_float(p[j + 2]), __uint_as_float(p[j + 3]));
-            __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(p[j + 4]), __uint_as_float(p[j + 5]));
-            __nv_bfloat162 h3 = __floats2bfloat162_rn(__uint_as_float(p[j + 6]), __uint_as_float(p[j + 7]));
-            v.x = *reinterpret_cast<uint32_t*>(&h0);
-            v.y = *reinterpret_cast<uint32_t*>(&h1);
-            v.z = *reinterpret_cast<uint32_t*>(&h2);
-            v.w = *reinterpret_cast<uint32_t*>(&h3);
-          }
+          __nv_bfloat162 h0 = __floats2bfloat162_rn(__uint_as_float(p[j + 0]), __uint_as_float(p[j + 1]));
+          __nv_bfloat162 h1 = __floats2bfloat162_rn(__uint_as_float(p[j + 2]), __uint_as_float(p[j + 3]));
+          __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(p[j + 4]), __uint_as_float(p[j + 5]));
+          __nv_bfloat162 h3 = __floats2bfloat162_rn(__uint_as_float(p[j + 6]), __uint_as_float(p[j + 7]));
+          v.x = *reinterpret_cast<uint32_t*>(&h0);
+          v.y = *reinterpret_cast<uint32_t*>(&h1);
+          v.z = *reinterpret_cast<uint32_t*>(&h2);
+          v.w = *reinterpret_cast<uint32_t*>(&h3);
           *reinterpret_cast<uint4*>(yrow + j) = v;
         }
       }
