@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   uint16_t* sAct = sBase + C::kBaseBytes / 2;
   uint8_t* sTok = reinterpret_cast<uint8_t*>(sAct + C::kActBytes / 2);
   __shared__ int s_count[2][kFewMaxExperts / 32];                                  // per 32 experts: active, pairs
+  __shared__ int s_active;                                                         // experts with tokens
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kTokWarp0 = C::kEpiWarps, kTmaWarp = kTokWarp0 + 4, kMmaWarp = kTmaWarp + 1;
@@ -359,72 +360,122 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     tmem_relinquish();
   }
 
-  // GateUp reads the routing that the preceding grid may have written, and
-  // lets Down start as soon as every CTA here has passed its wait: Down's
-  // CTAs then request weights while the last CTAs here finish.  For Down the
-  // routing is complete before it starts (GateUp waited for it), so only H
-  // and the output wait for GateUp.
-  if (MODE == kFewGateUp) griddep_wait();
+  // GateUp from bf16 rows reads the routing that the preceding grid may have
+  // written, and lets Down start as soon as every CTA here has passed its
+  // wait: Down's CTAs then request weights while the last CTAs here finish.
+  // GateUp from codes follows the quantizer, which started after all earlier
+  // work: the routing and the weights are there, only the codes are not.  So
+  // for Down the routing is complete before it starts, and only H and the
+  // output wait for GateUp.
+  if (MODE == kFewGateUp && kBf16) griddep_wait();
   griddep_launch_dependents();                    // the others' dependents wait before they touch memory
-  int active = 1;
   if constexpr (kMoe) {
     // sMask[e]: the tokens routed to e; sAct: the experts with any, ascending;
     // pair sBase[e] + i: e's i-th token, its weight the sum over the token's
     // slots that name e
     const int P = p.T * p.topk;
-    for (int e = tid; e < p.E; e += C::kThreads) sMask[e] = 0;
     if constexpr (MODE == kFewDown)
       for (int i = tid; i < NT * 128; i += C::kThreads) sAcc[i] = 0.0f;
-    __syncthreads();
-    for (int i = tid; i < P; i += C::kThreads) {
-      const int id = __ldg(p.ids + i);
-      if (id >= 0 && id < p.E) atomicOr(sMask + id, Mask(1) << (i / p.topk));
-      if (id >= p.E && blockIdx.x == 0) record_status(kDevBadExpert);
-    }
-    __syncthreads();
-    const int chunks = (p.E + 31) >> 5;
-    auto mask_of = [&](int e) { return e < p.E ? sMask[e] : Mask(0); };
-    for (int c = warp; c < chunks; c += C::kThreads / 32) {
-      const int k = __popcll(mask_of(c * 32 + lane));
-      const uint32_t on = __ballot_sync(0xFFFFFFFFu, k != 0);
-      const int pairs = __reduce_add_sync(0xFFFFFFFFu, k);
-      if (lane == 0) s_count[0][c] = __popc(on), s_count[1][c] = pairs;
-    }
-    __syncthreads();
-    for (int c = warp; c < chunks; c += C::kThreads / 32) {
-      const int k = __popcll(mask_of(c * 32 + lane));
-      const uint32_t on = __ballot_sync(0xFFFFFFFFu, k != 0);
-      int incl = k;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-        if (lane >= d) incl += o;
+    if (NT == 16 && P <= 32) {
+      // one warp, a lane per slot, no shared-memory passes (the general form's
+      // five took 2 us of a single token's 75)
+      if (warp == kTmaWarp) {
+        const int id = lane < P ? __ldg(p.ids + lane) : -1;
+        const float w = MODE == kFewDown && lane < P ? __ldg(p.wts + lane) : 0.0f;
+        const int t = lane / p.topk;
+        const bool in = id >= 0 && id < p.E;
+        if (id >= p.E && blockIdx.x == 0) record_status(kDevBadExpert);
+        const uint32_t below = (1u << lane) - 1u;
+        const uint32_t ins = __ballot_sync(0xFFFFFFFFu, in);
+        const uint32_t same_e = __match_any_sync(0xFFFFFFFFu, id) & ins;              // slots of this expert
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, id * 32 + t) & same_e;    // and of this token (t < 32)
+        const bool first = in && (same & below) == 0u;
+        const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
+        const bool leads = in && (same_e & below) == 0u;
+        const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
+        const int count = __popc(same_e & firsts);
+        int a = 0, base = 0;                     // experts and pairs before this one
+        float sum = 0.0f;
+        uint32_t tokens = 0u;
+        for (int o = 0; o < P; ++o) {
+          const int id_o = __shfl_sync(0xFFFFFFFFu, id, o), n_o = __shfl_sync(0xFFFFFFFFu, count, o);
+          const int t_o = __shfl_sync(0xFFFFFFFFu, t, o);
+          const float w_o = __shfl_sync(0xFFFFFFFFu, w, o);
+          const bool less = ((leaders >> o) & 1u) && id_o < id;
+          a += less ? 1 : 0;
+          base += less ? n_o : 0;
+          tokens |= ((same_e >> o) & 1u) << t_o;
+          if ((same >> o) & 1u) sum += w_o;
+        }
+        if (leads) {
+          sAct[a] = static_cast<uint16_t>(id);
+          sBase[id] = static_cast<uint16_t>(base);
+          sMask[id] = tokens;
+        }
+        if (first) {
+          const int at = base + __popc(same_e & firsts & below);
+          sTok[at] = static_cast<uint8_t>(t);
+          if constexpr (MODE == kFewDown) sWt[at] = sum;
+        }
+        if (lane == 0) s_active = __popc(leaders);
       }
-      // chunks before this one (at most 16)
-      const int na = __reduce_add_sync(0xFFFFFFFFu, lane < c ? s_count[0][lane & 15] : 0);
-      const int np = __reduce_add_sync(0xFFFFFFFFu, lane < c ? s_count[1][lane & 15] : 0);
-      if (k != 0) {
-        sAct[na + __popc(on & ((1u << lane) - 1u))] = static_cast<uint16_t>(c * 32 + lane);
-        sBase[c * 32 + lane] = static_cast<uint16_t>(np + incl - k);
+    } else {
+      for (int e = tid; e < p.E; e += C::kThreads) sMask[e] = 0;
+      __syncthreads();
+      for (int i = tid; i < P; i += C::kThreads) {
+        const int id = __ldg(p.ids + i);
+        if (id >= 0 && id < p.E) atomicOr(sMask + id, Mask(1) << (i / p.topk));
+        if (id >= p.E && blockIdx.x == 0) record_status(kDevBadExpert);
       }
-    }
-    __syncthreads();
-    active = __reduce_add_sync(0xFFFFFFFFu, lane < chunks ? s_count[0][lane & 15] : 0);
-    for (int i = tid; i < P; i += C::kThreads) {
-      const int id = __ldg(p.ids + i);
-      if (id < 0 || id >= p.E) continue;
-      const int t = i / p.topk, j = i - t * p.topk;
-      bool first = true;
-      for (int k = 0; k < j; ++k) first = first && __ldg(p.ids + t * p.topk + k) != id;
-      if (!first) continue;
-      const int at = sBase[id] + __popcll(sMask[id] & bits_below<Mask>(t));
-      FGFP8_DCHECK(at < C::kPairs);
-      sTok[at] = static_cast<uint8_t>(t);
-      if constexpr (MODE == kFewDown) {
-        float w = __ldg(p.wts + i);
-        for (int k = j + 1; k < p.topk; ++k)
-          if (__ldg(p.ids + t * p.topk + k) == id) w += __ldg(p.wts + t * p.topk + k);
-        sWt[at] = w;
+      __syncthreads();
+      const int chunks = (p.E + 31) >> 5;
+      auto mask_of = [&](int e) { return e < p.E ? sMask[e] : Mask(0); };
+      for (int c = warp; c < chunks; c += C::kThreads / 32) {
+        const int k = __popcll(mask_of(c * 32 + lane));
+        const uint32_t on = __ballot_sync(0xFFFFFFFFu, k != 0);
+        const int pairs = __reduce_add_sync(0xFFFFFFFFu, k);
+        if (lane == 0) s_count[0][c] = __popc(on), s_count[1][c] = pairs;
+      }
+      __syncthreads();
+      for (int c = warp; c < chunks; c += C::kThreads / 32) {
+        const int k = __popcll(mask_of(c * 32 + lane));
+        const uint32_t on = __ballot_sync(0xFFFFFFFFu, k != 0);
+        int incl = k;
+  #pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+          if (lane >= d) incl += o;
+        }
+        // chunks before this one (at most 16)
+        const int na = __reduce_add_sync(0xFFFFFFFFu, lane < c ? s_count[0][lane & 15] : 0);
+        const int np = __reduce_add_sync(0xFFFFFFFFu, lane < c ? s_count[1][lane & 15] : 0);
+        if (k != 0) {
+          sAct[na + __popc(on & ((1u << lane) - 1u))] = static_cast<uint16_t>(c * 32 + lane);
+          sBase[c * 32 + lane] = static_cast<uint16_t>(np + incl - k);
+        }
+      }
+      __syncthreads();
+      if (tid == 0) {
+        int all = 0;
+        for (int c = 0; c < chunks; ++c) all += s_count[0][c];
+        s_active = all;
+      }
+      for (int i = tid; i < P; i += C::kThreads) {
+        const int id = __ldg(p.ids + i);
+        if (id < 0 || id >= p.E) continue;
+        const int t = i / p.topk, j = i - t * p.topk;
+        bool first = true;
+        for (int k = 0; k < j; ++k) first = first && __ldg(p.ids + t * p.topk + k) != id;
+        if (!first) continue;
+        const int at = sBase[id] + __popcll(sMask[id] & bits_below<Mask>(t));
+        FGFP8_DCHECK(at < C::kPairs);
+        sTok[at] = static_cast<uint8_t>(t);
+        if constexpr (MODE == kFewDown) {
+          float w = __ldg(p.wts + i);
+          for (int k = j + 1; k < p.topk; ++k)
+            if (__ldg(p.ids + t * p.topk + k) == id) w += __ldg(p.wts + t * p.topk + k);
+          sWt[at] = w;
+        }
       }
     }
   }
@@ -433,7 +484,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   tc_fence_after();
   if (S > 1) cluster_arrive();                    // this CTA's barriers exist; the promotion warps wait for the others'
   const uint32_t tmem_base = *tmem_slot;
-  FewIter<MODE> work(p, active, sAct, rank, cluster, clusters);
+  FewIter<MODE> work(p, kMoe ? s_active : 1, sAct, rank, cluster, clusters);
   FewSeg sg{};
   auto count_of = [&](const FewSeg& s) -> int {   // tokens of a segment
     if constexpr (kMoe) return __popcll(sMask[s.e]);
@@ -443,7 +494,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     if constexpr (kMoe) return sBase[s.e];
     return 0;
   };
-  const bool weights_early = MODE == kFewDown || (MODE == kFewLinear && p.early);
+  const bool weights_early = MODE == kFewDown || (MODE == kFewGateUp && !kBf16) || (MODE == kFewLinear && p.early);
   if (!(warp == kTmaWarp && weights_early)) griddep_wait();
 
   if (warp == kTmaWarp) {
@@ -678,6 +729,17 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           }
           float* sc = sSc + (mine % C::kScSlots) * C::kTiles * NT;
           uint8_t* tile = sB + s * C::kBBytes;
+          // the rows first: their latency and the scales' overlap
+          if (MODE == kFewGateUp) {
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n * 128));
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < kTok; ++q)
+              if (q * 32 + lane < n) tma_load_2d(tile + (q * 32 + lane) * 128, &tmX, &full[s], kb * 128, tok[q]);
+          } else if (lane == 0) {
+            mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n16 * 2048));
+            for (int c = 0; c < n16; ++c) tma_load_2d(tile + c * 2048, &tmX, &full[s], kb * 128, pair0 + c * 16);
+          }
 #pragma unroll
           for (int q = 0; q < kTok; ++q) {
             const int i = q * 32 + lane;
@@ -687,21 +749,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
               for (int t = 0; t < C::kTiles; ++t) sc[t * NT + i] = a * scale_value(sw[t], p.fmt);
             }
           }
-          if (MODE == kFewGateUp) {
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n * 128));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sc_full[mine % C::kScSlots]);
-#pragma unroll
-            for (int q = 0; q < kTok; ++q)
-              if (q * 32 + lane < n) tma_load_2d(tile + (q * 32 + lane) * 128, &tmX, &full[s], kb * 128, tok[q]);
-          } else {
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&sc_full[mine % C::kScSlots]);
-              mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n16 * 2048));
-              for (int c = 0; c < n16; ++c) tma_load_2d(tile + c * 2048, &tmX, &full[s], kb * 128, pair0 + c * 16);
-            }
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[mine % C::kScSlots]);
           if (next < it_end) {
             load_sa(kb_of(next));
             load_sw(kb_of(next));

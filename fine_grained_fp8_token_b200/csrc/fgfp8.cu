@@ -697,13 +697,23 @@ fgfp8_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned th
   return ok();
 }
 
-// One few-token kernel.  `blocks`: the most pieces of work that K blocks are
-// not needed to make (128-row weight blocks, or pairs of an expert and a
-// block).  When they leave resident CTAs idle, K is split over clusters of
-// up to kMaxS CTAs; GateUp strides over its pieces with at most one resident
-// wave, the others launch one cluster per piece.
+// log2 of a few-token kernel's cluster size: `blocks` pieces of work (128-row
+// weight blocks, or pairs of an expert and a block) of at most `units` K
+// blocks each.  When the pieces leave resident CTAs idle, K is split over up
+// to kMaxS CTAs.
+template <int MODE, int NT>
+int few_lg_cluster(int64_t blocks, int64_t units, int sm_count) {
+  using C = fgfp8::FewCfg<MODE, NT>;
+  const int64_t slots = static_cast<int64_t>(sm_count) * C::kCtas;
+  int lg = 0;
+  while ((2 << lg) <= C::kMaxS && (blocks << (lg + 1)) <= slots && (2 << lg) <= units) ++lg;
+  return lg;
+}
+
+// One few-token kernel: GateUp strides over its pieces with at most one
+// resident wave, the others launch one cluster per piece.
 template <int MODE, int NT, bool kBf16>
-fgfp8_status launch_few(const uint8_t* W, uint64_t rows, uint64_t src_rows, fgfp8::FewArgs a, int64_t blocks,
+fgfp8_status launch_few(const uint8_t* W, uint64_t rows, uint64_t src_rows, fgfp8::FewArgs a, int64_t blocks, int lg,
                         cudaStream_t stream, int dev, int sm_count, const char* what) {
   using C = fgfp8::FewCfg<MODE, NT>;
   CUtensorMap mW, mX{};
@@ -719,8 +729,7 @@ fgfp8_status launch_few(const uint8_t* W, uint64_t rows, uint64_t src_rows, fgfp
   st = set_smem(reinterpret_cast<const void*>(kernel), C::kSmemBytes, dev);
   if (st != FGFP8_OK) return st;
   const int64_t slots = static_cast<int64_t>(sm_count) * C::kCtas;
-  a.lgS = 0;
-  while ((2 << a.lgS) <= C::kMaxS && (blocks << (a.lgS + 1)) <= slots && (2 << a.lgS) <= a.KB) ++a.lgS;
+  a.lgS = lg;
   int64_t clusters = blocks;
   if (MODE == fgfp8::kFewGateUp && clusters > (slots >> a.lgS)) clusters = slots >> a.lgS;
   return launch_cluster(kernel, static_cast<unsigned>(clusters << a.lgS), C::kThreads, C::kSmemBytes, 1 << a.lgS,
@@ -773,11 +782,14 @@ fgfp8_status few_linear(const void* src, int64_t ld_src, const void* Xs, int64_t
   a.epi = epi;
   a.early = early;
   const char* what = "few-token linear launch";
+  const uint64_t rows = static_cast<uint64_t>(N), src_rows = static_cast<uint64_t>(M);
   if (kBf16 || M <= 16)
-    return launch_few<fgfp8::kFewLinear, 16, kBf16>(Wq, static_cast<uint64_t>(N), static_cast<uint64_t>(M), a, a.NB, stream,
-                                                      dev, sm_count, what);
-  return launch_few<fgfp8::kFewLinear, 64, false>(Wq, static_cast<uint64_t>(N), static_cast<uint64_t>(M), a, a.NB, stream,
-                                                      dev, sm_count, what);
+    return launch_few<fgfp8::kFewLinear, 16, kBf16>(Wq, rows, src_rows, a, a.NB,
+                                                    few_lg_cluster<fgfp8::kFewLinear, 16>(a.NB, a.KB, sm_count), stream,
+                                                    dev, sm_count, what);
+  return launch_few<fgfp8::kFewLinear, 64, false>(Wq, rows, src_rows, a, a.NB,
+                                                  few_lg_cluster<fgfp8::kFewLinear, 64>(a.NB, a.KB, sm_count), stream,
+                                                  dev, sm_count, what);
 }
 
 // Dense GEMM with its epilogue; with dry set, only validates.
@@ -855,6 +867,9 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
   a.Hs = reinterpret_cast<float*>(ws + at.hs);
   a.I = static_cast<int>(I);
   const int64_t most = E < T * topk ? E : T * topk;            // experts that the tokens can meet
+  const int KB13 = static_cast<int>(K / 128), KB2 = static_cast<int>(I / 128);
+  const int lg13 = few_lg_cluster<fgfp8::kFewGateUp, NT>(most * KB2, KB13, sms);
+  const int lg2 = few_lg_cluster<fgfp8::kFewDown, NT>(KB13, most * KB2, sms);
   // gate/up: [E, 2I, K]
   a.src = X;
   a.ld_src = static_cast<uint64_t>(ldx);
@@ -868,24 +883,23 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
     a.ld_s = static_cast<uint64_t>(at.ld_s);
   }
   a.Ws = W13s;
-  a.KB = static_cast<int>(K / 128);
-  a.NB = static_cast<int>(2 * I / 128);
+  a.KB = KB13;
+  a.NB = 2 * KB2;
   st = launch_few<fgfp8::kFewGateUp, NT, kBf16>(W13q, static_cast<uint64_t>(E) * 2 * I, static_cast<uint64_t>(T), a,
-                                                most * (I / 128), s, dev, sms, "expert gate/up launch");
+                                                most * KB2, lg13, s, dev, sms, "expert gate/up launch");
   if (st != FGFP8_OK) return st;
   // down: [E, K, I]
   a.src = a.Hq;
   a.ld_src = static_cast<uint64_t>(I);
   a.src_scale = a.Hs;
   a.Ws = W2s;
-  a.KB = static_cast<int>(I / 128);
-  a.NB = static_cast<int>(K / 128);
+  a.KB = KB2;
+  a.NB = KB13;
   a.Y = reinterpret_cast<__nv_bfloat16*>(Y);
   a.N = static_cast<int>(K);
   a.epi = epi;
   return launch_few<fgfp8::kFewDown, NT, false>(W2q, static_cast<uint64_t>(E) * K, static_cast<uint64_t>(T) * topk, a,
-                                                a.NB, s, dev, sms,
-                                                "expert down launch");
+                                                a.NB, lg2, s, dev, sms, "expert down launch");
 }
 
 template <bool kSigmoid, typename In>
