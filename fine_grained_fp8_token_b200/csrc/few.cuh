@@ -346,8 +346,9 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     }
     for (int w = 0; w < 2; ++w) mbar_init(&mma_done[w], 1);
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&red_full[g], 4 * S);
-      mbar_init(&red_empty[g], 4 * S);
+      const int warps = MODE == kFewDown ? C::kEpiWarps : 4;         // Down: the groups meet together
+      mbar_init(&red_full[g], warps * S);
+      mbar_init(&red_empty[g], warps * S);
       mbar_init(&amax_bar[g], 4);
     }
     mbar_init(seg_bar, C::kEpiWarps);
@@ -694,7 +695,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       } else {
         // lane: the scales of tokens lane, lane + 32.  Lane 0 requests the rows
         // where they are contiguous, 16 at a time; GateUp's are anyone's rows
-        // of X, and each lane requests its own.
+        // of X, and lane g requests rows 4 g .. 4 g + 3 in one gather (the last
+        // token's again past the end).
         constexpr int kTok = (NT + 31) / 32;
         const int n16 = (n + 15) >> 4;
         uint32_t sa[kTok];
@@ -702,6 +704,12 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
 #pragma unroll
         for (int q = 0; q < kTok; ++q)
           tok[q] = MODE == kFewGateUp && q * 32 + lane < n ? sTok[pair0 + q * 32 + lane] : q * 32 + lane;
+        int four[4];
+        const int n4 = (n + 3) >> 2;
+        if constexpr (MODE == kFewGateUp) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) four[k] = sTok[pair0 + (4 * lane + k < n ? 4 * lane + k : n - 1)];
+        }
         auto load_sa = [&](int kb) {
 #pragma unroll
           for (int q = 0; q < kTok; ++q) {
@@ -731,11 +739,10 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           uint8_t* tile = sB + s * C::kBBytes;
           // the rows first: their latency and the scales' overlap
           if (MODE == kFewGateUp) {
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n * 128));
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n4 * 512));
             __syncwarp();
-#pragma unroll
-            for (int q = 0; q < kTok; ++q)
-              if (q * 32 + lane < n) tma_load_2d(tile + (q * 32 + lane) * 128, &tmX, &full[s], kb * 128, tok[q]);
+            if (lane < n4)
+              tma_gather4_2d(tile + lane * 512, &tmX, &full[s], kb * 128, four[0], four[1], four[2], four[3]);
           } else if (lane == 0) {
             mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n16 * 2048));
             for (int c = 0; c < n16; ++c) tma_load_2d(tile + c * 2048, &tmX, &full[s], kb * 128, pair0 + c * 16);
@@ -1022,15 +1029,52 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     if constexpr (MODE == kFewDown) {
       // the block's sums over all experts, residual added, one rounding
       if (C::kGroups > 1 && ok && segs > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(seg_bar, (segs - 1) & 1u))) expired();
+      if (C::kGroups > 1 && S > 1) {
+        // Many tokens: all of them meet at once in the stages, which are free
+        // when every rank has promoted its last block (eight at a time through
+        // sRed took 8 us for 64 tokens): [rank][slot][128] in sA, token t to
+        // rank t % S, slot t / S.
+        float* ring = reinterpret_cast<float*>(sA);
+        const int per = NT >> lgS;
+        cluster_wait();                                              // the others' barriers exist
+        if (ok && lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_empty[0]), lane));
+        if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_empty[0], 0))) expired();
+        if (ok) {
+#pragma unroll 4
+          for (int t = grp; t < p.T; t += C::kGroups)
+            st_cluster_f32(map_to_rank(smem_u32(ring + (rank * per + (t >> lgS)) * 128 + row), t & (S - 1)),
+                           sAcc[t * 128 + row]);
+          __syncwarp();
+          if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_full[0]), lane));
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_full[0], 0))) expired();
+        }
+        meets = 1;
 #pragma unroll 1
-      for (int c = 0; c < kSubs && sub0(c) < p.T && ok; ++c) {
-        float x[1][C::kRedTok];
+        for (int c = 0; c < kSubs && sub0(c) < p.T && ok; ++c) {
+          float x[C::kRedTok];
 #pragma unroll
-        for (int q = 0; q < C::kRedTok; ++q) x[0][q] = sAcc[(sub0(c) + q) * 128 + row];
-        if (S > 1) meet(x, p.T - sub0(c));
-        if (!ok) break;
-        if (c > 0) load_res(c);
-        finish_rows(c, x[0]);
+          for (int k = 0; k < C::kRedTok; ++k) x[k] = 0.0f;
+          const float* from = ring + (sub0(c) >> lgS) * 128 + row;
+#pragma unroll 1
+          for (int r = 0; r < S; ++r) {
+#pragma unroll
+            for (int k = 0; k < C::kRedTok / 2; ++k)                 // S >= 2
+              if (k < slots) x[k] += from[(r * per + k) * 128];
+          }
+          if (c > 0) load_res(c);
+          finish_rows(c, x);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kSubs && sub0(c) < p.T && ok; ++c) {
+          float x[1][C::kRedTok];
+#pragma unroll
+          for (int q = 0; q < C::kRedTok; ++q) x[0][q] = sAcc[(sub0(c) + q) * 128 + row];
+          if (S > 1) meet(x, p.T - sub0(c));
+          if (!ok) break;
+          if (c > 0) load_res(c);
+          finish_rows(c, x[0]);
+        }
       }
     }
     if (S > 1 && meets == 0) cluster_wait();
