@@ -400,7 +400,7 @@ ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _ACT_CODES = frozenset(_ACTS.values())
 _SCORES = {"softmax": 0, "sigmoid": 1}
-FUSED_QUANT_TOKENS = 16       # linear_epilogue needs no Xq / Xs up to this many tokens
+FUSED_QUANT_TOKENS = 8        # linear_epilogue needs no Xq / Xs up to this many tokens
 MOE_MAX_TOKENS = 64
 
 

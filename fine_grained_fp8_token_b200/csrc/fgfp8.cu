@@ -762,7 +762,10 @@ fgfp8::EpiArgs make_epilogue(const void* bias, int bias_type, int act, const voi
 }
 
 // The few-token linear kernel (M <= 64): from bf16 rows X (kBf16), or from
-// codes and scales.
+// codes and scales.  The narrow tile up to 8 tokens: with more, its token
+// warps or its one promotion group fall behind the weights (18432 x 7168, with
+// the quantizer: 8 tokens 27.2 us quantizing inside, 26.9 from codes; 16
+// tokens 31.0 and 28.7; the wide tile 26.4 for 17; one token 24.0, 25.9).
 template <bool kBf16>
 fgfp8_status few_linear(const void* src, int64_t ld_src, const void* Xs, int64_t ld_s, const uint8_t* Wq,
                         const void* Ws, void* Y, int64_t M, int64_t N, int64_t K, int fmt, const fgfp8::EpiArgs& epi,
@@ -783,7 +786,7 @@ fgfp8_status few_linear(const void* src, int64_t ld_src, const void* Xs, int64_t
   a.early = early;
   const char* what = "few-token linear launch";
   const uint64_t rows = static_cast<uint64_t>(N), src_rows = static_cast<uint64_t>(M);
-  if (kBf16 || M <= 16)
+  if (kBf16 || M <= FGFP8_FUSED_QUANT_TOKENS)
     return launch_few<fgfp8::kFewLinear, 16, kBf16>(Wq, rows, src_rows, a, a.NB,
                                                     few_lg_cluster<fgfp8::kFewLinear, 16>(a.NB, a.KB, sm_count), stream,
                                                     dev, sm_count, what);
@@ -824,7 +827,7 @@ fgfp8_status gemm_epilogue_impl(const uint8_t* Xq, const void* Xs, int64_t ld_s,
 }
 
 // Workspace of fgfp8_moe_decode: codes of H [T * topk, I] and its scales, and
-// for more than FGFP8_FUSED_QUANT_TOKENS tokens the codes and scales of X.
+// for more than FGFP8_MOE_FUSED_TOKENS tokens the codes and scales of X.
 struct MoeWorkspace {
   int64_t hs, xq, xs, bytes;         // offsets, and the whole size
   int64_t ld_s;
@@ -833,7 +836,7 @@ struct MoeWorkspace {
     hs = up(T * topk * I);
     xq = up(hs + T * topk * (I / 128) * 4);
     ld_s = (T + 15) / 16 * 16;
-    const bool quant = T > FGFP8_FUSED_QUANT_TOKENS;
+    const bool quant = T > FGFP8_MOE_FUSED_TOKENS;
     xs = quant ? up(xq + T * K) : xq;
     bytes = quant ? xs + ld_s * (K / 128) * 4 : xq;
   }
@@ -1335,7 +1338,7 @@ fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, co
   const fgfp8::EpiArgs epi = make_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (T <= FGFP8_FUSED_QUANT_TOKENS)
+  if (T <= FGFP8_MOE_FUSED_TOKENS)
     return launch_moe<16, true>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
                           info.sm_count);
   return launch_moe<64, false>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,

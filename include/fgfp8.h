@@ -251,7 +251,7 @@ fgfp8_status fgfp8_grouped_linear(const void* X, int64_t ldx, uint8_t* Xq, void*
  * FGFP8_FUSED_QUANT_TOKENS: it then quantizes X inside the GEMM, and Xq and
  * Xs may be NULL.  Within act, NaN stays NaN.
  */
-#define FGFP8_FUSED_QUANT_TOKENS 16
+#define FGFP8_FUSED_QUANT_TOKENS 8
 
 fgfp8_status fgfp8_gemm_epilogue(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq, const void* Ws,
                                  void* Y, int64_t M, int64_t N, int64_t K, int fmt, const void* bias, int bias_type,
@@ -295,7 +295,7 @@ fgfp8_status fgfp8_route_topk(const void* logits, int logits_type, int64_t ld, c
 
 /*
  * A whole SwiGLU expert layer for a few tokens (decode), in two kernels up to
- * FGFP8_FUSED_QUANT_TOKENS tokens and with the quantizer before them above;
+ * FGFP8_MOE_FUSED_TOKENS tokens and with the quantizer before them above;
  * the grouped and masked calls above serve larger batches.  For token t:
  *   (g, u) = W13[e] x_hat          x_hat: fgfp8_quant_act of x_t
  *   h      = silu(g) * u           in fp32, quantized per 1x128 group straight
@@ -326,6 +326,7 @@ fgfp8_status fgfp8_route_topk(const void* logits, int logits_type, int64_t ld, c
  * depend on the order of ids within other tokens or on timing.
  */
 #define FGFP8_MOE_MAX_TOKENS 64
+#define FGFP8_MOE_FUSED_TOKENS 16
 
 /* *bytes (host memory): the workspace of fgfp8_moe_decode at these sizes. */
 fgfp8_status fgfp8_moe_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t* bytes);
