@@ -17,6 +17,7 @@ one.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -443,14 +444,25 @@ def _dense(t, where: str, name: str, dtypes, shape, dev: int) -> None:
 def _check_weight(Wq, Ws, where, fmt, dev, names=("Wq", "Ws"), dims=2):
     """Checks a stack of block-quantized weights; returns its shape."""
     t = _t
-    if fmt != SCALE_F32 and fmt != SCALE_UE8M0:
-        _refuse(where, "fmt must be SCALE_F32 (0) or SCALE_UE8M0 (1)")
     shape = Wq.shape
-    if len(shape) != dims or shape[-1] % 128 or shape[-2] % 128:
-        _refuse(where, f"{names[0]} must have {dims} dimensions, the last two multiples of 128", 2)
+    if len(shape) != dims:
+        _refuse(where, f"{names[0]} must have {dims} dimensions", 2)
+    if dims == 2:
+        N, K = shape
+        blocks = (N // 128, K // 128)
+    else:
+        E, N, K = shape
+        blocks = (E, N // 128, K // 128)
+    if N % 128 or K % 128:
+        _refuse(where, f"the last two dimensions of {names[0]} must be multiples of 128", 2)
+    if fmt == SCALE_F32:
+        sdtypes = (t.float32,)
+    elif fmt == SCALE_UE8M0:
+        sdtypes = (t.uint8,)
+    else:
+        _refuse(where, "fmt must be SCALE_F32 (0) or SCALE_UE8M0 (1)")
     _dense(Wq, where, names[0], (t.uint8, t.float8_e4m3fn), shape, dev)
-    _dense(Ws, where, names[1], (t.float32,) if fmt == SCALE_F32 else (t.uint8,),
-           (*shape[:-2], shape[-2] // 128, shape[-1] // 128), dev)
+    _dense(Ws, where, names[1], sdtypes, blocks, dev)
     return shape
 
 
@@ -595,8 +607,9 @@ def route_topk(logits, topk: int, score: str = "softmax", bias=None, n_group: in
     return _run_on(dev, stream, where, call)
 
 
+@functools.lru_cache(maxsize=256)
 def moe_workspace_bytes(T: int, topk: int, K: int, I: int) -> int:
-    """Bytes of moe_decode's workspace."""
+    """Bytes of moe_decode's workspace (a function of these sizes alone)."""
     n = ctypes.c_int64()
     _check(fgfp8_moe_workspace_bytes(T, topk, K, I, ctypes.byref(n)), "fgfp8_moe_workspace_bytes")
     return n.value

@@ -908,13 +908,14 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
 template <bool kSigmoid, typename In>
 fgfp8_status launch_route(const fgfp8::RouteArgs& a, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>((a.T + fgfp8::kRouteWarps - 1) / fgfp8::kRouteWarps);
-  const unsigned threads = fgfp8::kRouteWarps * 32;
-  if (a.E <= 32) fgfp8::route_topk_kernel<1, kSigmoid, In><<<grid, threads, 0, s>>>(a);
-  else if (a.E <= 64) fgfp8::route_topk_kernel<2, kSigmoid, In><<<grid, threads, 0, s>>>(a);
-  else if (a.E <= 128) fgfp8::route_topk_kernel<4, kSigmoid, In><<<grid, threads, 0, s>>>(a);
-  else if (a.E <= 256) fgfp8::route_topk_kernel<8, kSigmoid, In><<<grid, threads, 0, s>>>(a);
-  else fgfp8::route_topk_kernel<16, kSigmoid, In><<<grid, threads, 0, s>>>(a);
-  return check_launch("route_topk launch");
+  auto go = [&](auto kernel) {
+    return launch_dependent(kernel, grid, fgfp8::kRouteWarps * 32, 0, s, "route_topk launch", a);
+  };
+  if (a.E <= 32) return go(fgfp8::route_topk_kernel<1, kSigmoid, In>);
+  if (a.E <= 64) return go(fgfp8::route_topk_kernel<2, kSigmoid, In>);
+  if (a.E <= 128) return go(fgfp8::route_topk_kernel<4, kSigmoid, In>);
+  if (a.E <= 256) return go(fgfp8::route_topk_kernel<8, kSigmoid, In>);
+  return go(fgfp8::route_topk_kernel<16, kSigmoid, In>);
 }
 
 }  // namespace

@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(const Rout
   __shared__ int s_sel[kRouteWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int t = blockIdx.x * kRouteWarps + w;
+  griddep_launch_dependents();
+  griddep_wait();                             // the scores may be the preceding grid's
   if (t >= p.T) return;
   const In* row = reinterpret_cast<const In*>(p.logits) + static_cast<uint64_t>(t) * p.ld;
   const int e0 = lane * EPL;

@@ -298,6 +298,70 @@ def test_attention_output_router_and_experts_together(dev):
     check(Y, *reference(x, ri, w.cpu().numpy(), W, fmt, x))
 
 
+@pytest.mark.parametrize("T", [1, 12, 40])
+def test_the_step_replayed_back_to_back(dev, T):
+    """Output projection, router and two expert layers captured in one graph
+    and replayed without a wait between the replays: each kernel may start
+    while the one before it ends, and the results are those of the calls made
+    one at a time."""
+    E, topk, K, I, fmt = 128, 4, 512, 256, UE8M0
+    Woq, Wos = fg.quant_weight(workloads.weights((K, K), seed=3).to(dev), fmt)
+    Wgq, Wgs = fg.quant_weight(workloads.weights((E, K), seed=4, std=0.3).to(dev), fmt)
+    W = weights_for(dev, E, K, I, fmt, seed=500)
+
+    def step(a, r, wait):
+        def after(x):
+            if wait:
+                torch.cuda.synchronize()
+            return x
+        x = after(fg.linear_epilogue(a, Woq, Wos, fmt, residual=r))
+        for _ in range(2):
+            logits = after(fg.linear_epilogue(x, Wgq, Wgs, fmt))
+            ids, w = after(fg.route_topk(logits, topk, score="sigmoid"))
+            x = after(fg.moe_decode(x, ids, w, *W, fmt, residual=x))
+        return x
+    inputs = [[workloads.activations((T, K), "normal", seed=10 * s + j).to(dev) for j in (0, 1)] for s in range(4)]
+    alone = [step(a, r, True) for a, r in inputs]
+    a, r = (torch.zeros_like(t) for t in inputs[0])
+    step(a, r, True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(a, r, False)
+    got = []
+    for i in range(12):
+        a.copy_(inputs[i % 4][0]), r.copy_(inputs[i % 4][1])
+        graph.replay()
+        got.append(out.clone())
+    eager = [step(*inputs[i % 4], False) for i in range(8)]
+    torch.cuda.synchronize()
+    fg.check_device_status()
+    for i, y in enumerate(got):
+        assert torch.equal(y, alone[i % 4]), i
+    for i, y in enumerate(eager):
+        assert torch.equal(y, alone[i % 4]), i
+
+
+def test_two_streams_with_workspaces_of_their_own(dev):
+    """Two expert layers at once on two streams give what they give alone."""
+    T, E, topk, K, I, fmt = 6, 16, 4, 512, 256, F32
+    W = weights_for(dev, E, K, I, fmt, seed=600)
+    calls = []
+    for s in range(2):
+        X = workloads.activations((T, K), "normal", seed=s).to(dev)
+        ids, w = route(T, E, topk, seed=s)
+        calls.append((X, ids.to(dev), w.to(dev)))
+    alone = [fg.moe_decode(*c, *W, fmt) for c in calls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(30):
+        outs.append((i % 2, fg.moe_decode(*calls[i % 2], *W, fmt, stream=streams[i % 2])))
+    torch.cuda.synchronize()
+    fg.check_device_status()
+    for i, y in outs:
+        assert torch.equal(y, alone[i])
+
+
 def test_zero_tokens(dev):
     W = weights_for(dev, 2, 128, 128, F32, seed=1)
     X = torch.empty(0, 128, dtype=torch.bfloat16, device=dev)
