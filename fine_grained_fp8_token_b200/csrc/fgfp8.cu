@@ -736,8 +736,20 @@ fgfp8_status launch_few(const uint8_t* W, uint64_t rows, uint64_t src_rows, fgfp
                         stream, what, mW, mX, a);
 }
 
-// Checks of the epilogue's arguments for an [M, N] output.
-fgfp8_status check_epilogue(const void* bias, int bias_type, int act, const void* residual, int64_t ld_r, int64_t N) {
+constexpr char kInputMeetsOutput[] = "X must not overlap Y: it may be read while Y is written";
+
+// Whether the spans of two bf16 matrices, first to last element, share memory.
+bool spans_meet(const void* a, int64_t a_rows, int64_t a_cols, int64_t a_ld, const void* b, int64_t b_rows,
+                int64_t b_cols, int64_t b_ld) {
+  if (a_rows <= 0 || b_rows <= 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + 2 * static_cast<uintptr_t>((b_rows - 1) * b_ld + b_cols) &&
+         b0 < a0 + 2 * static_cast<uintptr_t>((a_rows - 1) * a_ld + a_cols);
+}
+
+// Checks of the epilogue's arguments for an [M, N] output Y.
+fgfp8_status check_epilogue(const void* bias, int bias_type, int act, const void* residual, int64_t ld_r,
+                            const void* Y, int64_t M, int64_t N) {
   if (act < FGFP8_ACT_NONE || act > FGFP8_ACT_GELU_TANH)
     return fail(FGFP8_ERR_INVALID_ARG, "act must be one of fgfp8_act (0..4)");
   if (bias_type != FGFP8_BF16 && bias_type != FGFP8_F32)
@@ -747,6 +759,8 @@ fgfp8_status check_epilogue(const void* bias, int bias_type, int act, const void
     if (ld_r < N) return fail(FGFP8_ERR_SHAPE, "ld_r must be >= the output's row length");
     if (!aligned(residual, 16) || ld_r % 8 != 0)
       return fail(FGFP8_ERR_ALIGN, "residual must be 16-byte aligned with ld_r % 8 == 0");
+    if (!(residual == Y && (ld_r == N || M == 1)) && spans_meet(residual, M, N, ld_r, Y, M, N, N))
+      return fail(FGFP8_ERR_INVALID_ARG, "residual must be Y itself or not overlap it");
   }
   return FGFP8_OK;
 }
@@ -802,7 +816,7 @@ fgfp8_status gemm_epilogue_impl(const uint8_t* Xq, const void* Xs, int64_t ld_s,
   if (M == 0 && fmt >= 0 && fmt <= 1 && N >= 0 && K >= 0) return ok();
   fgfp8_status st = check_gemm_common(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt);
   if (st != FGFP8_OK) return st;
-  st = check_epilogue(bias, bias_type, act, residual, ld_r, N);
+  st = check_epilogue(bias, bias_type, act, residual, ld_r, Y, M, N);
   if (st != FGFP8_OK) return st;
   if (dry) return FGFP8_OK;
   int dev;
@@ -1227,8 +1241,9 @@ fgfp8_status fgfp8_linear_epilogue(const void* X, int64_t ldx, uint8_t* Xq, void
     if (!aligned(X, 16) || ldx % 8 != 0) return fail(FGFP8_ERR_ALIGN, "X must be 16-byte aligned with ldx % 8 == 0");
     if (!aligned(Wq, 16) || !aligned(Y, 16)) return fail(FGFP8_ERR_ALIGN, "Wq and Y must be 16-byte aligned");
     if (fmt == FGFP8_SCALE_F32 && !aligned(Ws, 4)) return fail(FGFP8_ERR_ALIGN, "fp32 Ws must be 4-byte aligned");
-    st = check_epilogue(bias, bias_type, act, residual, ld_r, N);
+    st = check_epilogue(bias, bias_type, act, residual, ld_r, Y, M, N);
     if (st != FGFP8_OK) return st;
+    if (spans_meet(X, M, K, ldx, Y, M, N, N)) return fail(FGFP8_ERR_INVALID_ARG, kInputMeetsOutput);
     int dev;
     DeviceInfo info;
     st = current_device(&dev, &info);
@@ -1241,6 +1256,7 @@ fgfp8_status fgfp8_linear_epilogue(const void* X, int64_t ldx, uint8_t* Xq, void
   if (st != FGFP8_OK) return st;
   st = gemm_epilogue_impl(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt, bias, bias_type, act, residual, ld_r, stream, 1, true);
   if (st != FGFP8_OK) return st;
+  if (spans_meet(X, M, K, ldx, Y, M, N, N)) return fail(FGFP8_ERR_INVALID_ARG, kInputMeetsOutput);
   st = quant_act_impl(X, M, K, ldx, Xq, Xs, ld_s, fmt, stream, false);
   if (st != FGFP8_OK) return st;
   return gemm_epilogue_impl(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt, bias, bias_type, act, residual, ld_r, stream, 1,
@@ -1330,7 +1346,7 @@ fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, co
   if (!aligned(workspace, 256)) return fail(FGFP8_ERR_ALIGN, "workspace must be 256-byte aligned");
   if (workspace_bytes < MoeWorkspace(T, topk, K, I).bytes)
     return fail(FGFP8_ERR_SHAPE, "workspace_bytes is below fgfp8_moe_workspace_bytes");
-  st = check_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r, K);
+  st = check_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r, Y, T, K);
   if (st != FGFP8_OK) return st;
   int dev;
   DeviceInfo info;

@@ -244,8 +244,8 @@ fgfp8_status fgfp8_grouped_linear(const void* X, int64_t ldx, uint8_t* Xq, void*
  *   act        an fgfp8_act.
  *   residual   bf16 [M, N], row stride ld_r elements (ld_r >= N, ld_r % 8 ==
  *              0, 16-byte aligned); NULL: none (ld_r is then ignored).  It may
- *              be Y itself (ld_r == N), and must not overlap Y in any other
- *              way.
+ *              be Y itself (ld_r == N); otherwise the spans of the two, first
+ *              to last element, must not overlap, nor may those of X and Y.
  * The other arguments are those of fgfp8_gemm / fgfp8_linear, except that
  * fgfp8_linear_epilogue neither reads nor writes Xq and Xs when M <=
  * FGFP8_FUSED_QUANT_TOKENS: it then quantizes X inside the GEMM, and Xq and

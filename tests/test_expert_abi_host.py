@@ -13,7 +13,7 @@ A = 1 << 20          # a fake, 256-byte aligned "device" address; never derefere
 
 
 def linear(**kw):
-    a = dict(X=A, ldx=256, Xq=A, Xs=A, ld_s=4, Wq=A, Ws=A, Y=A, M=4, N=128, K=256, fmt=0, bias=None, bias_type=0, act=0,
+    a = dict(X=A << 2, ldx=256, Xq=A, Xs=A, ld_s=4, Wq=A, Ws=A, Y=A, M=4, N=128, K=256, fmt=0, bias=None, bias_type=0, act=0,
              residual=None, ld_r=0)
     a.update(kw)
     return fg.fgfp8_linear_epilogue(*a.values(), None)
@@ -27,7 +27,7 @@ def gemm(**kw):
 
 
 EPILOGUE = [(dict(act=5), INVALID), (dict(act=-1), INVALID), (dict(bias_type=2), INVALID), (dict(bias=A + 2), ALIGN),
-            (dict(residual=A, ld_r=120), SHAPE), (dict(residual=A, ld_r=132), ALIGN), (dict(residual=A + 8, ld_r=128), ALIGN),
+            (dict(residual=A << 2, ld_r=120), SHAPE), (dict(residual=A, ld_r=132), ALIGN), (dict(residual=A + 8, ld_r=128), ALIGN),
             (dict(Wq=None), INVALID), (dict(Y=None), INVALID), (dict(Y=A + 4), ALIGN), (dict(Ws=A + 2), ALIGN),
             (dict(fmt=2), INVALID), (dict(N=100), SHAPE), (dict(N=0), SHAPE), (dict(K=200, ldx=200), SHAPE),
             (dict(K=0), SHAPE), (dict(N=-128), INVALID)]
@@ -41,6 +41,24 @@ def test_epilogue_refusals(M, bad, code):
     kw.pop("ldx", None)
     assert gemm(**kw) == code, bad
     assert fg.fgfp8_last_error_string() != ""
+
+
+def test_overlaps_are_refused():
+    far = A + (1 << 24)
+    for M in (1, 4, 40, 400):
+        kw = dict(M=M, ld_s=400, X=far, Xq=far, Xs=far)
+        # the residual may be Y itself, row by row, and nothing else that meets it
+        assert linear(**kw, residual=A, ld_r=128) == gemm(M=M, ld_s=400, residual=A, ld_r=128)
+        if not torch.cuda.is_available():
+            assert linear(**kw, residual=A, ld_r=128) == CUDA
+            assert linear(**kw, residual=A + 2 * M * 128, ld_r=128) == CUDA
+        if M > 1:
+            assert linear(**kw, residual=A, ld_r=256) == INVALID
+            assert gemm(M=M, ld_s=400, residual=A + 256, ld_r=128) == INVALID
+        assert linear(**kw, residual=A + 16, ld_r=128) == INVALID
+        assert linear(M=M, ld_s=400, X=A) == INVALID                       # X is Y
+        assert linear(M=M, ld_s=400, X=A - 2 * M * 256 + 32, Y=A) == INVALID
+    assert moe(X=far, residual=A + 512, ld_r=256) == INVALID
 
 
 def test_linear_epilogue_operand_refusals():

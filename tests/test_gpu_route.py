@@ -39,7 +39,8 @@ def reference(z, topk, score, bias, G, keep, renorm, scale):
             if m == -np.inf:
                 p = np.zeros(E)
             else:
-                p = np.where(z[t] == m, 1.0, np.exp(np.where(z[t] == m, 0.0, z[t] - m)))
+                with np.errstate(invalid="ignore"):           # inf - inf where z is the maximum itself
+                    p = np.where(z[t] == m, 1.0, np.exp(np.where(z[t] == m, 0.0, z[t] - m)))
                 p = p / p.sum()
         else:
             with np.errstate(over="ignore"):
