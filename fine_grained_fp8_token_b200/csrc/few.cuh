@@ -227,42 +227,52 @@ struct FewSeg {
   int a, e;                         // position in the active list, expert
   int j;                            // GateUp: 128-wide block of I; else the 128-row block of N
   int kb0, kb1;
+  bool joint;                       // the cluster's ranks share the piece, each a part of its K
 };
 
 // The segments of one CTA, the same sequence for every role.
-//   GateUp  items (a, j) strided over the clusters, rank r taking its S-th of K
+//   GateUp  items (a, j), each CTA one of its own per round.  What is left for
+//           the last round, if it is at most one item per cluster, the ranks
+//           share: r takes the r-th of S parts of K (512 items on 148 CTAs: the
+//           last round of 68 took as long as a full one)
 //   Down    the cluster's block of 128 output columns: the (a, kb) blocks of
 //           all active experts in one line, cut into S equal ranges
 //   Linear  the cluster's block of 128 output columns, rank r its S-th of K
 template <int MODE>
 struct FewIter {
-  int pos, end, step, KB, NJ, j, kb0, kb1;
+  int pos, end, KB, NJ, j, rank, lgS, cluster, ctas;
   const uint16_t* act;
-  __device__ FewIter(const FewArgs& p, int active, const uint16_t* act_, int rank, int cluster, int clusters) {
+  __device__ FewIter(const FewArgs& p, int active, const uint16_t* act_, int rank_, int cluster_) {
     act = act_;
     KB = p.KB;
     NJ = p.I / 128;
-    j = cluster;
+    j = cluster = cluster_;
+    rank = rank_;
+    lgS = p.lgS;
+    ctas = gridDim.x;
+    pos = 0, end = 1;
     if (MODE == kFewGateUp) {
-      pos = cluster, end = active * NJ, step = clusters;
-      kb0 = KB * rank >> p.lgS, kb1 = KB * (rank + 1) >> p.lgS;
+      end = active * NJ;                              // items; pos: the round's first
     } else if (MODE == kFewDown) {
       const int units = active * KB;                  // at most 2^9 experts x 2^13 blocks
-      pos = units * rank >> p.lgS;
-      end = units * (rank + 1) >> p.lgS;
-    } else {
-      pos = 0, end = 1;
-      kb0 = KB * rank >> p.lgS, kb1 = KB * (rank + 1) >> p.lgS;
+      pos = units * rank >> lgS;
+      end = units * (rank + 1) >> lgS;
     }
   }
   __device__ bool next(FewSeg& s) {
     if (pos >= end) return false;
+    s.joint = true;
     if (MODE == kFewGateUp) {
-      s.a = pos / NJ;
-      s.j = pos - s.a * NJ;
+      const int left = end - pos;
+      s.joint = left <= ctas >> lgS && lgS > 0;
+      const int mine = s.joint ? cluster : (cluster << lgS) + rank;
+      if (mine >= left) return false;
+      s.a = (pos + mine) / NJ;
+      s.j = pos + mine - s.a * NJ;
       s.e = act[s.a];
-      s.kb0 = kb0, s.kb1 = kb1;
-      pos += step;
+      s.kb0 = s.joint ? KB * rank >> lgS : 0;
+      s.kb1 = s.joint ? KB * (rank + 1) >> lgS : KB;
+      pos += s.joint ? left : ctas;
     } else if (MODE == kFewDown) {
       s.a = pos / KB;
       s.e = act[s.a];
@@ -271,7 +281,8 @@ struct FewIter {
       s.kb1 = s.kb0 + (end - pos) < KB ? s.kb0 + (end - pos) : KB;
       pos += s.kb1 - s.kb0;
     } else {
-      s.a = 0, s.e = 0, s.j = j, s.kb0 = kb0, s.kb1 = kb1;
+      s.a = 0, s.e = 0, s.j = j;
+      s.kb0 = KB * rank >> lgS, s.kb1 = KB * (rank + 1) >> lgS;
       pos = end;
     }
     return true;
@@ -332,7 +343,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   constexpr int kTokWarp0 = C::kEpiWarps, kTmaWarp = kTokWarp0 + 4, kMmaWarp = kTmaWarp + 1;
   const int lgS = p.lgS, S = 1 << lgS;
   const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int cluster = static_cast<int>(blockIdx.x) >> lgS, clusters = static_cast<int>(gridDim.x) >> lgS;
+  const int cluster = static_cast<int>(blockIdx.x) >> lgS;
 
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -485,7 +496,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
   tc_fence_after();
   if (S > 1) cluster_arrive();                    // this CTA's barriers exist; the promotion warps wait for the others'
   const uint32_t tmem_base = *tmem_slot;
-  FewIter<MODE> work(p, kMoe ? s_active : 1, sAct, rank, cluster, clusters);
+  FewIter<MODE> work(p, kMoe ? s_active : 1, sAct, rank, cluster);
   FewSeg sg{};
   auto count_of = [&](const FewSeg& s) -> int {   // tokens of a segment
     if constexpr (kMoe) return __popcll(sMask[s.e]);
@@ -774,7 +785,9 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
     float* red = sRed + grp * (C::kRedBytes / C::kGroups / 4);
     constexpr int kSubs = C::kChunks * 16 / C::kRedTok;              // meetings of a full tile
-    const int slots = C::kRedTok >> lgS;                             // tokens of a meeting per rank
+    // How the current piece's tokens are shared: by the cluster's ranks, or (a
+    // GateUp item of this CTA alone) not at all.
+    int slots = C::kRedTok >> lgS, lgW = lgS, who = rank;            // tokens of a meeting per rank
     uint32_t it = 0, pairs = 0, meets = 0, segs = 0, quants = 0;
     bool ok = true;
     auto expired = [&] {
@@ -784,10 +797,10 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     // first token of this group's chunk q, and of its meeting c
     auto chunk0 = [&](int q) { return (q * C::kGroups + grp) * 16; };
     auto sub0 = [&](int c) { return chunk0(c * C::kRedTok / 16) + c * C::kRedTok % 16; };
-    // A rank's token in slot k of a meeting is rank + k S (S divides kRedTok).
+    // A rank's token in slot k of a meeting is who + k 2^lgW (2^lgW divides kRedTok).
     auto own_of = [&](int c, int n) {                                // slots with a token below n
-      const int left = n - sub0(c) - rank;
-      const int k = left <= 0 ? 0 : (left + S - 1) >> lgS;
+      const int left = n - sub0(c) - who;
+      const int k = left <= 0 ? 0 : (left + (1 << lgW) - 1) >> lgW;
       return k < slots ? k : slots;
     };
 
@@ -874,6 +887,11 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     float acc[C::kChunks][C::kTiles][16];
     while (ok && work.next(sg)) {
       const int n = count_of(sg), pair0 = pair0_of(sg);
+      if (MODE == kFewGateUp) {
+        lgW = sg.joint ? lgS : 0;
+        who = sg.joint ? rank : 0;
+        slots = C::kRedTok >> lgW;
+      }
 #pragma unroll
       for (int q = 0; q < C::kChunks; ++q)
 #pragma unroll
@@ -976,7 +994,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
 #pragma unroll
                 for (int q = 0; q < C::kRedTok; ++q) x[t][q] = acc[(cc * C::kRedTok + q) / 16][t][(cc * C::kRedTok + q) % 16];
             }
-          if (S > 1) meet(x, n - sub0(c));
+          if (lgW > 0) meet(x, n - sub0(c));
           if (!ok) break;
           if constexpr (MODE == kFewLinear) {
             if (c > 0) load_res(c);
@@ -1003,8 +1021,8 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
                 break;
               }
               ++quants;
-              const uint64_t r0 = static_cast<uint64_t>(pair0 + sub0(c) + rank);
-              FGFP8_DCHECK(r0 + ((own - 1) << lgS) < static_cast<uint64_t>(p.T) * p.topk && sg.j * 128 + row < p.I);
+              const uint64_t r0 = static_cast<uint64_t>(pair0 + sub0(c) + who);
+              FGFP8_DCHECK(r0 + ((own - 1) << lgW) < static_cast<uint64_t>(p.T) * p.topk && sg.j * 128 + row < p.I);
 #pragma unroll
               for (int k = 0; k < C::kRedTok; ++k) {
                 // magnitude bits compare like the values, and a NaN above all of them
@@ -1012,7 +1030,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
                 float inv;
                 const float scale = scale_of_f32(__uint_as_float(max(max(m4.x, m4.y), max(m4.z, m4.w))), p.fmt, inv);
                 const uint8_t code = quant_f32(h[k], scale, inv);
-                const uint64_t r = r0 + (static_cast<uint64_t>(k) << lgS);
+                const uint64_t r = r0 + (static_cast<uint64_t>(k) << lgW);
                 if (k < own) {
                   p.Hq[r * p.I + sg.j * 128 + row] = code;
                   if (row == 0) p.Hs[r * (p.I / 128) + sg.j] = scale;

@@ -885,7 +885,9 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
   a.I = static_cast<int>(I);
   const int64_t most = E < T * topk ? E : T * topk;            // experts that the tokens can meet
   const int KB13 = static_cast<int>(K / 128), KB2 = static_cast<int>(I / 128);
-  const int lg13 = few_lg_cluster<fgfp8::kFewGateUp, NT>(most * KB2, KB13, sms);
+  // at least pairs of CTAs, so that they can share the last round's items
+  int lg13 = few_lg_cluster<fgfp8::kFewGateUp, NT>(most * KB2, KB13, sms);
+  if (lg13 == 0 && KB13 >= 2) lg13 = 1;
   const int lg2 = few_lg_cluster<fgfp8::kFewDown, NT>(KB13, most * KB2, sms);
   // gate/up: [E, 2I, K]
   a.src = X;
