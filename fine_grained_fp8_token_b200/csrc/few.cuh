@@ -849,12 +849,12 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
 
     // Output rows (Linear, Down): this rank's tokens of meeting c, all in
     // flight together (one token after the other took 500 cycles each).  Their
-    // residuals are loaded ahead: the first meeting's before the K loop.
+    // residuals are loaded a meeting ahead, the first one's before the K loop.
     const int col = (MODE == kFewGateUp ? 0 : cluster) * 128 + row;
     float bias = 0.0f;
-    uint16_t res[C::kRedTok];
+    uint16_t res[C::kRedTok];                                        // of the meeting to come
     auto load_res = [&](int c) {
-      const int own = own_of(c, p.T);
+      const int own = c < kSubs ? own_of(c, p.T) : 0;
       const uint16_t* from = reinterpret_cast<const uint16_t*>(p.epi.residual) +
                              static_cast<uint64_t>(sub0(c) + rank) * p.epi.ld_r + col;
 #pragma unroll
@@ -871,13 +871,14 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
         for (int k = 0; k < C::kRedTok; ++k) x[k] += bias;
         apply_act_n(x, p.epi.act);
       }
+#pragma unroll
+      for (int k = 0; k < C::kRedTok; ++k) x[k] += __uint_as_float(static_cast<uint32_t>(res[k]) << 16);
+      load_res(c + 1);
       FGFP8_DCHECK(col < p.N && (own == 0 || sub0(c) + rank + ((own - 1) << lgS) < p.T));
       __nv_bfloat16* to = p.Y + static_cast<uint64_t>(sub0(c) + rank) * p.N + col;
 #pragma unroll
       for (int k = 0; k < C::kRedTok; ++k)
-        if (k < own)
-          to[(static_cast<uint64_t>(k) << lgS) * p.N] =
-              __float2bfloat16_rn(x[k] + __uint_as_float(static_cast<uint32_t>(res[k]) << 16));
+        if (k < own) to[(static_cast<uint64_t>(k) << lgS) * p.N] = __float2bfloat16_rn(x[k]);
     };
     if constexpr (MODE != kFewGateUp) {
       load_res(0);
@@ -997,7 +998,6 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           if (lgW > 0) meet(x, n - sub0(c));
           if (!ok) break;
           if constexpr (MODE == kFewLinear) {
-            if (c > 0) load_res(c);
             finish_rows(c, x[0]);
           } else {
             // h = silu(g) u in fp32, its 1x128 group (the 128 threads' rows)
@@ -1079,7 +1079,6 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             for (int k = 0; k < C::kRedTok / 2; ++k)                 // S >= 2
               if (k < slots) x[k] += from[(r * per + k) * 128];
           }
-          if (c > 0) load_res(c);
           finish_rows(c, x);
         }
       } else {
@@ -1090,7 +1089,6 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
           for (int q = 0; q < C::kRedTok; ++q) x[0][q] = sAcc[(sub0(c) + q) * 128 + row];
           if (S > 1) meet(x, p.T - sub0(c));
           if (!ok) break;
-          if (c > 0) load_res(c);
           finish_rows(c, x[0]);
         }
       }
