@@ -13,21 +13,29 @@
 //   promotion   (4 or 8 warps) thread = weight row; per 128-wide K block the
 //               partial of each token from TMEM times sa * sw into fp32
 //               accumulators, then the epilogue;
-//   tokens      (4 warps) each K block belongs to one of them in turn: from bf16 rows it gathers the
-//               expert's token rows, quantizes them and writes the 128-byte-
-//               swizzled tile; it requests rows of codes from the TMA; in both
-//               cases it writes the products sa * sw.
-//               The rows are L2-resident, and quantizing them again per weight
-//               block costs a few instructions per 16 KB of weights, which
-//               saves a quantizer kernel and the gather of rows.  One warp per
-//               block, so that four blocks' loads overlap: the proxy fence
-//               before a block is handed over waits for all of its thread's
-//               loads (measured with all four warps on every block: 87 us
-//               for M = 37, N = 18432, K = 7168);
-//   TMA         (1 warp) the weight tiles and, where the source is codes, the
-//               token rows (a linear layer's rows are contiguous, and an
-//               expert's rows of H are);
+//   tokens      (4 warps) the token operand of the K blocks in their stages and
+//               the products sa * sw.  Up to 16 tokens GateUp (8: Linear)
+//               reads bf16 rows, quantizes them and writes the 128-byte-
+//               swizzled tile: the rows are L2-resident, and quantizing them
+//               again per weight block costs few instructions per 16 KB of
+//               weights and saves a kernel.  One warp per block, so that the
+//               blocks' loads overlap: the proxy fence before a block is
+//               handed over waits for its thread's loads (all four warps on
+//               every block: 87 us at 37 x 18432 x 7168, one warp each: 52).
+//               With more tokens that arithmetic falls behind the weights
+//               (64 tokens x 32 experts: 395 us, from codes 282), so the rows
+//               come as codes, by TMA: 16 contiguous rows a copy, or gathered
+//               four at a time for an expert's tokens;
+//   TMA         (1 warp) the weight tiles;
 //   MMA         (1 or 2 warps) owns TMEM, issues the MMAs.
+//
+// Measured (one B200, back to back in a CUDA graph, weights read once at the
+// measured 6.57 TB/s as the floor): 1 token x 8 of 256 experts of 7168 x 2048
+// 70 us (floor 53.7), 7 tokens 353 (342), 64 tokens x 32 experts 257 (215);
+// linear 1 x 4096 x 4096 7.0 us (2.6), 37 x 18432 x 7168 28 us (20.4).  What
+// remains is the start (launch, routing, the first weights' latency: 5 to 8
+// us), the gate/up kernel's end (its last epilogues and the hand-over, 5 us),
+// and with few blocks the ranks' meeting (2 us).
 //
 // Few rows leave fewer 128-row weight blocks than SMs, so K is split over the
 // CTAs of a cluster.  Their partial sums meet in distributed shared memory:
@@ -58,7 +66,7 @@ constexpr int kFewMaxTopk = 16;
 struct FewArgs {
   const void* src;                  // token operand: bf16 rows (ld_src in elements) or E4M3 codes (bytes)
   uint64_t ld_src;
-  const void* src_scale;            // codes only: Down fp32 [pair, KB], Linear MN-major [KB, ld_s] in `fmt`
+  const void* src_scale;            // codes only: Down fp32 [pair, KB], else MN-major [KB, ld_s] in `fmt`
   uint64_t ld_s;
   const void* Ws;                   // weight block scales in `fmt`
   int fmt;
@@ -117,7 +125,8 @@ struct FewCfg {
   static constexpr int kCtas = NT == 16 ? 2 : 1;
   static constexpr uint32_t kBudget = (kCtas == 2 ? 115712u : 232448u) - 1024u;     // after the 1 KB alignment
   static constexpr uint32_t kFixed =
-      kScSlots * kScBytes + kRedBytes + kAccBytes + kMaskBytes + kBaseBytes + kActBytes + kTokBytes + kWeightBytes + kAmaxBytes + kBarrierBytes;
+      kScSlots * kScBytes + kRedBytes + kAccBytes + kMaskBytes + kBaseBytes + kActBytes + kTokBytes + kWeightBytes +
+      kAmaxBytes + kBarrierBytes;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
   static constexpr int kStagesFit = static_cast<int>((kBudget - kFixed) / kStageBytes);
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
@@ -135,7 +144,8 @@ struct FewCfg {
   static constexpr uint32_t kTmemCols = kNumBuf * kBufCols;                          // 64 to 512
   // Issuing a block's MMAs, commits and waits takes one warp about 480
   // cycles.  Alone on its SM a CTA wants a block every 540 to 700, so two
-  // warps take the pairs in turn.
+  // warps take the pairs in turn (64 tokens x 32 experts: 298 us with one,
+  // 283 with two).
   static constexpr int kMmaWarps = NT == 64 ? 2 : 1;
   static constexpr int kThreads = (kEpiWarps + 5 + kMmaWarps) * 32;
   static_assert(kStages >= 3, "pipeline depth");

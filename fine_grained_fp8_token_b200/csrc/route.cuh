@@ -19,7 +19,9 @@
 // lowest index; the winner drops its head.  Which of its experts that was is
 // found for all slots together at the end.  The kernel is bound by issuing
 // instructions (about 15 a round and 100 around them), not by its 4 E bytes
-// per token.
+// per token: 8192 tokens x 256 experts in 8 groups with a bias 16 us, 20011 x
+// 160 softmax 11 us, one token 3.7 us (selecting with a lane's maximum and
+// 64-bit shuffles took 49, 27 and 14).
 //
 // sigma(z) + bias is defined in 64 bits.  The warp forms it in 32 and looks at
 // the gaps its decisions rest on; where one is within the 32-bit error, it
