@@ -405,13 +405,18 @@ FUSED_QUANT_TOKENS = 8        # linear_epilogue needs no Xq / Xs up to this many
 MOE_MAX_TOKENS = 64
 
 
-_t = None                     # torch, imported with the first call
+# torch and the dtypes the checks compare with, bound with the first call.
+_t = None
+_CODES = _F32 = _U8 = _I32 = _BF16 = _BIAS = ()
 
 
 def _torch():
-    global _t
+    global _t, _CODES, _F32, _U8, _I32, _BF16, _BIAS
     if _t is None:
         import torch
+        _CODES = (torch.uint8, torch.float8_e4m3fn)
+        _F32, _U8, _I32, _BF16 = (torch.float32,), (torch.uint8,), (torch.int32,), (torch.bfloat16,)
+        _BIAS = (torch.bfloat16, torch.float32)
         _t = torch
     return _t
 
@@ -420,7 +425,8 @@ def _refuse(where: str, message: str, status: int = 1):
     raise FGFP8Error(status, where, message)
 
 
-# The checks run on every call, so they build no message until one is needed.
+# The checks run on every call (host time is what a small call costs), so they
+# build no message until one is needed.
 def _matrix(t, where: str, name: str, dtype, dev: int) -> int:
     """Checks a row-major matrix operand on device index dev; returns its row
     stride."""
@@ -443,7 +449,6 @@ def _dense(t, where: str, name: str, dtypes, shape, dev: int) -> None:
 
 def _check_weight(Wq, Ws, where, fmt, dev, names=("Wq", "Ws"), dims=2):
     """Checks a stack of block-quantized weights; returns its shape."""
-    t = _t
     shape = Wq.shape
     if len(shape) != dims:
         _refuse(where, f"{names[0]} must have {dims} dimensions", 2)
@@ -455,45 +460,51 @@ def _check_weight(Wq, Ws, where, fmt, dev, names=("Wq", "Ws"), dims=2):
         blocks = (E, N // 128, K // 128)
     if N % 128 or K % 128:
         _refuse(where, f"the last two dimensions of {names[0]} must be multiples of 128", 2)
-    if fmt == SCALE_F32:
-        sdtypes = (t.float32,)
-    elif fmt == SCALE_UE8M0:
-        sdtypes = (t.uint8,)
-    else:
+    if fmt != SCALE_F32 and fmt != SCALE_UE8M0:
         _refuse(where, "fmt must be SCALE_F32 (0) or SCALE_UE8M0 (1)")
-    _dense(Wq, where, names[0], (t.uint8, t.float8_e4m3fn), shape, dev)
-    _dense(Ws, where, names[1], sdtypes, blocks, dev)
+    _dense(Wq, where, names[0], _CODES, shape, dev)
+    _dense(Ws, where, names[1], _F32 if fmt == SCALE_F32 else _U8, blocks, dev)
     return shape
 
 
-def _run_on(dev: int, stream, where: str, call):
-    """call(stream handle) with device index `dev` current; what it allocates
-    belongs to the stream it launches on."""
+class _On:
+    """The device of index dev and, if given, the stream as the current ones, so
+    that what a call allocates belongs to the stream it launches on."""
+
+    def __init__(self, dev: int, stream, where: str):
+        if stream is not None and stream.device.index != dev:
+            _refuse(where, f"the stream must be on device {dev}")
+        self.contexts = [_t.cuda.device(dev)] + ([] if stream is None else [_t.cuda.stream(stream)])
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _launch_stream(dev: int, where: str) -> int:
     if dev < 0:
         _refuse(where, "the tensors must be on a CUDA device")
-    cuda = _t.cuda
-    if stream is None and dev == cuda.current_device():
-        return call(_t._C._cuda_getCurrentRawStream(dev))
-    with cuda.device(dev):
-        if stream is None:
-            return call(_t._C._cuda_getCurrentRawStream(dev))
-        if stream.device.index != dev:
-            _refuse(where, f"the stream must be on device {dev}")
-        with cuda.stream(stream):
-            return call(int(stream.cuda_stream))
+    return _t._C._cuda_getCurrentRawStream(dev)
+
+
+def _is_elsewhere(dev: int, stream) -> bool:
+    return dev >= 0 and (stream is not None or dev != _t.cuda.current_device())
 
 
 def _epilogue_args(where, M, N, dev, bias, act, residual):
-    t = _t
     code = _ACTS.get(act) if isinstance(act, str) else act
     if code not in _ACT_CODES:
         _refuse(where, f"act must be one of {sorted(_ACTS)} or its code")
     bp, bt, rp, ld_r = None, 0, None, N
     if bias is not None:
-        _dense(bias, where, "bias", (t.bfloat16, t.float32), (N,), dev)
-        bp, bt = bias.data_ptr(), int(bias.dtype is t.float32)
+        _dense(bias, where, "bias", _BIAS, (N,), dev)
+        bp, bt = bias.data_ptr(), int(bias.dtype is _t.float32)
     if residual is not None:
-        ld_r = _matrix(residual, where, "residual", t.bfloat16, dev)
+        ld_r = _matrix(residual, where, "residual", _t.bfloat16, dev)
         if residual.shape != (M, N):
             _refuse(where, f"residual must be [{M}, {N}]", 2)
         rp = residual.data_ptr()
@@ -508,23 +519,25 @@ def gemm_epilogue(Xq, Xs, Wq, Ws, fmt: int, bias=None, act="none", residual=None
     Y."""
     where, t = "gemm_epilogue", _torch()
     dev = Xq.get_device()
+    if _is_elsewhere(dev, stream):
+        with _On(dev, stream, where):
+            return gemm_epilogue(Xq, Xs, Wq, Ws, fmt, bias, act, residual, Y)
     N, K = _check_weight(Wq, Ws, where, fmt, dev)
     M = Xq.shape[0]
-    _dense(Xq, where, "Xq", (t.uint8, t.float8_e4m3fn), (M, K), dev)
-    _dense(Xs, where, "Xs", (t.float32,) if fmt == SCALE_F32 else (t.uint8,), (K // 128, Xs.shape[-1]), dev)
+    _dense(Xq, where, "Xq", _CODES, (M, K), dev)
+    ld_s = Xs.shape[-1]
+    _dense(Xs, where, "Xs", _F32 if fmt == SCALE_F32 else _U8, (K // 128, ld_s), dev)
     epi = _epilogue_args(where, M, N, dev, bias, act, residual)
     if Y is not None:
-        _dense(Y, where, "Y", (t.bfloat16,), (M, N), dev)
-    lib = load()
-
-    def call(s):
-        out = Xq.new_empty((M, N), dtype=t.bfloat16) if Y is None else Y
-        st = lib.fgfp8_gemm_epilogue(Xq.data_ptr(), Xs.data_ptr(), Xs.shape[1], Wq.data_ptr(), Ws.data_ptr(),
-                                     out.data_ptr(), M, N, K, fmt, *epi, s)
-        if st:
-            _check(st, "fgfp8_gemm_epilogue")
-        return out
-    return _run_on(dev, stream, where, call)
+        _dense(Y, where, "Y", _BF16, (M, N), dev)
+    s = _launch_stream(dev, where)
+    if Y is None:
+        Y = Xq.new_empty((M, N), dtype=t.bfloat16)
+    st = load().fgfp8_gemm_epilogue(Xq.data_ptr(), Xs.data_ptr(), ld_s, Wq.data_ptr(), Ws.data_ptr(), Y.data_ptr(), M,
+                                    N, K, fmt, *epi, s)
+    if st:
+        _check(st, "fgfp8_gemm_epilogue")
+    return Y
 
 
 def linear_epilogue(X, Wq, Ws, fmt: int, bias=None, act="none", residual=None, Y=None, Xq=None, Xs=None,
@@ -532,41 +545,46 @@ def linear_epilogue(X, Wq, Ws, fmt: int, bias=None, act="none", residual=None, Y
     """The W8A8 linear layer with its epilogue, Y = bf16(act(X W^T + bias) +
     residual), from bf16 X [M, K] (any row stride that is a multiple of 8) and
     the pre-quantized weight.  Xq / Xs are the quantizer's buffers (allocated
-    here when not given, not needed for M <= FUSED_QUANT_TOKENS); bias, act and
-    residual as in gemm_epilogue.  Returns Y."""
+    here when not both given, not needed for M <= FUSED_QUANT_TOKENS); bias, act
+    and residual as in gemm_epilogue.  Returns Y."""
     where, t = "linear_epilogue", _torch()
     dev = X.get_device()
+    if _is_elsewhere(dev, stream):
+        with _On(dev, stream, where):
+            return linear_epilogue(X, Wq, Ws, fmt, bias, act, residual, Y, Xq, Xs, ld_s)
     N, K = _check_weight(Wq, Ws, where, fmt, dev)
     ldx = _matrix(X, where, "X", t.bfloat16, dev)
-    M = X.shape[0]
-    if X.shape[1] != K:
-        _refuse(where, f"X has {X.shape[1]} columns, Wq {K}", 2)
+    M, KX = X.shape
+    if KX != K:
+        _refuse(where, f"X has {KX} columns, Wq {K}", 2)
     epi = _epilogue_args(where, M, N, dev, bias, act, residual)
     if Y is not None:
-        _dense(Y, where, "Y", (t.bfloat16,), (M, N), dev)
-    ld = scale_rows(M, fmt) if ld_s is None else ld_s
-    sdtype = t.float32 if fmt == SCALE_F32 else t.uint8
+        _dense(Y, where, "Y", _BF16, (M, N), dev)
+    if ld_s is None:
+        ld_s = scale_rows(M, fmt)
     if Xq is not None:
-        _dense(Xq, where, "Xq", (t.uint8, t.float8_e4m3fn), (M, K), dev)
+        _dense(Xq, where, "Xq", _CODES, (M, K), dev)
     if Xs is not None:
-        _dense(Xs, where, "Xs", (sdtype,), (K // 128, ld), dev)
-    lib = load()
-
-    def call(s):
-        out = X.new_empty((M, N)) if Y is None else Y
-        q, sc = Xq, Xs
-        if M > FUSED_QUANT_TOKENS:
-            if q is None:
-                q = X.new_empty((M, K), dtype=t.uint8)
-            if sc is None:
-                sc = X.new_empty((K // 128, ld), dtype=sdtype)
-        st = lib.fgfp8_linear_epilogue(X.data_ptr(), ldx, None if q is None else q.data_ptr(),
-                                       None if sc is None else sc.data_ptr(), ld, Wq.data_ptr(), Ws.data_ptr(),
-                                       out.data_ptr(), M, N, K, fmt, *epi, s)
-        if st:
-            _check(st, "fgfp8_linear_epilogue")
-        return out
-    return _run_on(dev, stream, where, call)
+        _dense(Xs, where, "Xs", _F32 if fmt == SCALE_F32 else _U8, (K // 128, ld_s), dev)
+    s = _launch_stream(dev, where)
+    if Y is None:
+        Y = X.new_empty((M, N))
+    q = scales = None
+    if M > FUSED_QUANT_TOKENS:
+        if Xq is None or Xs is None:      # one buffer: the codes, then the scales from a 256-byte boundary
+            codes = (M * K + 255) // 256 * 256
+            scratch = X.new_empty((codes + K // 128 * ld_s * (4 if fmt == SCALE_F32 else 1),), dtype=t.uint8)
+            q = scratch.data_ptr()
+            scales = q + codes
+        if Xq is not None:
+            q = Xq.data_ptr()
+        if Xs is not None:
+            scales = Xs.data_ptr()
+    st = load().fgfp8_linear_epilogue(X.data_ptr(), ldx, q, scales, ld_s, Wq.data_ptr(), Ws.data_ptr(), Y.data_ptr(),
+                                      M, N, K, fmt, *epi, s)
+    if st:
+        _check(st, "fgfp8_linear_epilogue")
+    return Y
 
 
 def route_topk(logits, topk: int, score: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
@@ -578,8 +596,11 @@ def route_topk(logits, topk: int, score: str = "softmax", bias=None, n_group: in
     weight 0.  Returns (ids int32 [T, topk], weights fp32 [T, topk])."""
     where, t = "route_topk", _torch()
     dev = logits.get_device()
+    if _is_elsewhere(dev, stream):
+        with _On(dev, stream, where):
+            return route_topk(logits, topk, score, bias, n_group, topk_group, renormalize, scale, ids, weights)
     dtype = logits.dtype
-    if dtype is not t.float32 and dtype is not t.bfloat16:
+    if dtype not in _BIAS:
         _refuse(where, "logits must be bf16 or fp32")
     ld = _matrix(logits, where, "logits", dtype, dev)
     T, E = logits.shape
@@ -587,24 +608,24 @@ def route_topk(logits, topk: int, score: str = "softmax", bias=None, n_group: in
         _refuse(where, f"score must be one of {sorted(_SCORES)}")
     if topk < 1:
         _refuse(where, "topk must be at least 1", 2)
+    bp = None
     if bias is not None:
-        _dense(bias, where, "bias", (t.float32,), (E,), dev)
+        _dense(bias, where, "bias", _F32, (E,), dev)
+        bp = bias.data_ptr()
     if ids is not None:
-        _dense(ids, where, "ids", (t.int32,), (T, topk), dev)
+        _dense(ids, where, "ids", _I32, (T, topk), dev)
     if weights is not None:
-        _dense(weights, where, "weights", (t.float32,), (T, topk), dev)
-    lib = load()
-
-    def call(s):
-        i = logits.new_empty((T, topk), dtype=t.int32) if ids is None else ids
-        w = logits.new_empty((T, topk), dtype=t.float32) if weights is None else weights
-        st = lib.fgfp8_route_topk(logits.data_ptr(), int(dtype is t.float32), ld,
-                                  None if bias is None else bias.data_ptr(), T, E, topk, _SCORES[score], n_group,
-                                  topk_group, int(renormalize), scale, i.data_ptr(), w.data_ptr(), s)
-        if st:
-            _check(st, "fgfp8_route_topk")
-        return i, w
-    return _run_on(dev, stream, where, call)
+        _dense(weights, where, "weights", _F32, (T, topk), dev)
+    s = _launch_stream(dev, where)
+    if ids is None:
+        ids = logits.new_empty((T, topk), dtype=t.int32)
+    if weights is None:
+        weights = logits.new_empty((T, topk), dtype=t.float32)
+    st = load().fgfp8_route_topk(logits.data_ptr(), int(dtype is t.float32), ld, bp, T, E, topk, _SCORES[score],
+                                 n_group, topk_group, int(renormalize), scale, ids.data_ptr(), weights.data_ptr(), s)
+    if st:
+        _check(st, "fgfp8_route_topk")
+    return ids, weights
 
 
 @functools.lru_cache(maxsize=256)
@@ -621,21 +642,24 @@ def moe_decode(X, ids, weights, W13q, W13s, W2q, W2s, fmt: int, residual=None, Y
     [T, topk] as from route_topk, W13q [E, 2I, K] / W13s with gate and up
     interleaved (interleave_gate_up per expert), W2q [E, K, I] / W2s.
     Y[t] = bf16(residual[t] + sum_j weights[t, j] expert_{ids[t, j]}(X[t])).
-    workspace: uint8 tensor of moe_workspace_bytes(T, topk, K, I) (allocated here
-    when not given; calls that may overlap need their own).  Returns Y."""
+    workspace: uint8 tensor of moe_workspace_bytes(T, topk, K, I) (allocated
+    here when not given; calls that may overlap need their own).  Returns Y."""
     where, t = "moe_decode", _torch()
     dev = X.get_device()
+    if _is_elsewhere(dev, stream):
+        with _On(dev, stream, where):
+            return moe_decode(X, ids, weights, W13q, W13s, W2q, W2s, fmt, residual, Y, workspace)
     s13 = _check_weight(W13q, W13s, where, fmt, dev, ("W13q", "W13s"), 3)
     E, K, I = _check_weight(W2q, W2s, where, fmt, dev, ("W2q", "W2s"), 3)
     ldx = _matrix(X, where, "X", t.bfloat16, dev)
-    T = X.shape[0]
-    if X.shape[1] != K or s13 != (E, 2 * I, K):
+    T, KX = X.shape
+    if KX != K or s13 != (E, 2 * I, K):
         _refuse(where, "W13q must be [E, 2I, K] and W2q [E, K, I] with X [T, K]", 2)
     if ids.dim() != 2:
         _refuse(where, "ids must be [T, topk]", 2)
     topk = ids.shape[1]
-    _dense(ids, where, "ids", (t.int32,), (T, topk), dev)
-    _dense(weights, where, "weights", (t.float32,), (T, topk), dev)
+    _dense(ids, where, "ids", _I32, (T, topk), dev)
+    _dense(weights, where, "weights", _F32, (T, topk), dev)
     rp, ld_r = None, K
     if residual is not None:
         ld_r = _matrix(residual, where, "residual", t.bfloat16, dev)
@@ -643,22 +667,20 @@ def moe_decode(X, ids, weights, W13q, W13s, W2q, W2s, fmt: int, residual=None, Y
             _refuse(where, f"residual must be [{T}, {K}]", 2)
         rp = residual.data_ptr()
     if Y is not None:
-        _dense(Y, where, "Y", (t.bfloat16,), (T, K), dev)
-    need = moe_workspace_bytes(T, topk, K, I)
+        _dense(Y, where, "Y", _BF16, (T, K), dev)
     if workspace is not None:
-        _dense(workspace, where, "workspace", (t.uint8,), (workspace.numel(),), dev)
-    lib = load()
-
-    def call(s):
-        out = X.new_empty((T, K)) if Y is None else Y
-        ws = X.new_empty((need,), dtype=t.uint8) if workspace is None else workspace
-        st = lib.fgfp8_moe_decode(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), W13q.data_ptr(),
-                                  W13s.data_ptr(), W2q.data_ptr(), W2s.data_ptr(), rp, ld_r, out.data_ptr(),
-                                  ws.data_ptr(), ws.numel(), T, topk, E, K, I, fmt, s)
-        if st:
-            _check(st, "fgfp8_moe_decode")
-        return out
-    return _run_on(dev, stream, where, call)
+        _dense(workspace, where, "workspace", _U8, (workspace.numel(),), dev)
+    s = _launch_stream(dev, where)
+    if Y is None:
+        Y = X.new_empty((T, K))
+    if workspace is None:
+        workspace = X.new_empty((moe_workspace_bytes(T, topk, K, I),), dtype=t.uint8)
+    st = load().fgfp8_moe_decode(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), W13q.data_ptr(),
+                                 W13s.data_ptr(), W2q.data_ptr(), W2s.data_ptr(), rp, ld_r, Y.data_ptr(),
+                                 workspace.data_ptr(), workspace.numel(), T, topk, E, K, I, fmt, s)
+    if st:
+        _check(st, "fgfp8_moe_decode")
+    return Y
 
 
 def selftest_expired_wait(stream=None) -> None:

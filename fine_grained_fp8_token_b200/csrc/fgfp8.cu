@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstdio>
 #include <map>
@@ -232,7 +233,8 @@ fgfp8_status launch_gemm(const uint8_t* Xq, const void* Xs, int64_t ld_s, const 
   auto kernel = fgfp8::gemm_blockscaled_kernel<BN, CW, FMT, kGrouped, kFuse, kEpi>;
   st = set_smem(reinterpret_cast<const void*>(kernel), C::kSmemBytes, dev);
   if (st != FGFP8_OK) return st;
-  if (C::kRegSplit) {
+  static std::atomic<bool> split_checked{false};
+  if (C::kRegSplit && !split_checked.load(std::memory_order_relaxed)) {
     // setmaxnreg.inc waits until registers are free: the warpgroups' shares
     // must fit in what the block is launched with, or it would wait forever.
     cudaFuncAttributes fa{};
@@ -243,6 +245,7 @@ fgfp8_status launch_gemm(const uint8_t* Xq, const void* Xs, int64_t ld_s, const 
     if (after > launch)
       return fail(FGFP8_ERR_UNSUPPORTED, "register split exceeds the launch allocation (" + std::to_string(fa.numRegs) +
                                             " registers x " + std::to_string(C::kThreads) + " threads)");
+    split_checked.store(true, std::memory_order_relaxed);        // the same for every launch of this kernel
   }
   const int64_t tiles = ((M + C::kBM - 1) / C::kBM) * (N / BN);
   if (tiles == 0) return ok();

@@ -177,6 +177,26 @@ def test_side_stream_and_graph_replay(dev):
     fg.check_device_status()
 
 
+def test_callers_buffers(dev):
+    """The quantizer's buffers given whole, in part or not at all; the codes
+    and scales left in them are the quantizer's."""
+    M, N, K = 70, 256, 640
+    for fmt in (F32, UE8M0):
+        X, Wq, Ws, b, R = make(dev, M, N, K, fmt, torch.float32, True, seed=4)
+        kw = dict(bias=b.to(dev), act="relu", residual=R.to(dev))
+        Xd = X.to(dev)
+        ref = fg.linear_epilogue(Xd, Wq, Ws, fmt, **kw)
+        Xq, Xs = fg.quant_act(Xd, fmt)
+        ld = Xs.shape[1] + 32
+        for q, s in ((1, 0), (0, 1), (1, 1)):
+            bq = torch.empty_like(Xq) if q else None
+            bs = torch.empty((K // 128, ld), dtype=Xs.dtype, device=dev) if s else None
+            assert torch.equal(ref, fg.linear_epilogue(Xd, Wq, Ws, fmt, Xq=bq, Xs=bs, ld_s=ld, **kw))
+            assert bq is None or torch.equal(bq, Xq)
+            assert bs is None or torch.equal(bs[:, :M], Xs[:, :M])
+    fg.check_device_status()
+
+
 def test_empty(dev):
     Wq, Ws = fg.quant_weight(workloads.weights((256, 128), seed=1).to(dev), F32)
     assert fg.linear_epilogue(torch.empty(0, 128, dtype=torch.bfloat16, device=dev), Wq, Ws, F32).shape == (0, 256)
