@@ -201,3 +201,26 @@ def test_empty(dev):
     Wq, Ws = fg.quant_weight(workloads.weights((256, 128), seed=1).to(dev), F32)
     assert fg.linear_epilogue(torch.empty(0, 128, dtype=torch.bfloat16, device=dev), Wq, Ws, F32).shape == (0, 256)
     fg.check_device_status()
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0])
+def test_quantizing_inside_leaves_the_same_bits(dev, fmt):
+    """Up to FUSED_QUANT_TOKENS tokens the kernel quantizes X itself: the same
+    codes, scales, split and order of sums as from the quantizer's buffers, so
+    the same bits; rows with NaN and infinities end as they do there, and the
+    other rows are as if those were not among them."""
+    for M in (1, 5, fg.FUSED_QUANT_TOKENS):
+        X, Wq, Ws, b, R = make(dev, M, 384, 1152, fmt, torch.float32, True, seed=M)
+        kw = dict(bias=b.to(dev), act="gelu_tanh", residual=R.to(dev))
+        clean = fg.linear_epilogue(X.to(dev), Wq, Ws, fmt, **kw)
+        X[0, 130], X[M // 2, 1000] = float("nan"), float("-inf")
+        Xd = X.to(dev)
+        Xq, Xs = fg.quant_act(Xd, fmt)
+        got = fg.linear_epilogue(Xd, Wq, Ws, fmt, **kw)
+        ref = fg.gemm_epilogue(Xq, Xs, Wq, Ws, fmt, **kw)
+        assert got[0].isnan().all()
+        for m in range(M):
+            assert torch.equal(got[m].nan_to_num(1.5), ref[m].nan_to_num(1.5)) and torch.equal(got[m].isnan(), ref[m].isnan())
+            if m not in (0, M // 2):
+                assert torch.equal(got[m], clean[m])
+    fg.check_device_status()

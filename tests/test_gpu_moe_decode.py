@@ -367,3 +367,34 @@ def test_zero_tokens(dev):
     X = torch.empty(0, 128, dtype=torch.bfloat16, device=dev)
     Y = fg.moe_decode(X, torch.empty(0, 2, dtype=torch.int32, device=dev), torch.empty(0, 2, device=dev), *W, F32)
     assert Y.shape == (0, 128)
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0])
+@pytest.mark.parametrize("T", [7, 40])
+def test_tokens_that_are_not_finite_stay_alone(dev, T, fmt):
+    """A token with a NaN, one with an infinity: not finite themselves, and the
+    others' rows are as without them."""
+    E, topk, K, I = 5, 3, 384, 256
+    W = weights_for(dev, E, K, I, fmt, seed=6)
+    X = workloads.activations((T, K), "normal", seed=1)
+    R = workloads.activations((T, K), "normal", seed=2)
+    ids, w = route(T, E, topk, seed=3)
+    clean = run(dev, X, ids, w, W, fmt, R)
+    X[1, 200], X[T - 2, 7] = float("nan"), float("inf")
+    Y = run(dev, X, ids, w, W, fmt, R)
+    fg.check_device_status()
+    rest = [t for t in range(T) if t not in (1, T - 2)]
+    assert torch.equal(Y[rest], clean[rest])
+    assert not Y[1].isfinite().any() and not Y[T - 2].isfinite().any()
+
+
+def test_long_rows(dev):
+    """K and I far above the usual ones (hundreds of K blocks a piece), and
+    the narrowest layer against them."""
+    for T, K, I in ((2, 65536, 128), (20, 128, 32768)):
+        E, topk, fmt = 2, 2, F32
+        W = weights_for(dev, E, K, I, fmt, seed=2)
+        X = workloads.activations((T, K), "normal", seed=1)
+        ids, w = route(T, E, topk, seed=3)
+        check(run(dev, X, ids, w, W, fmt), *reference(X, ids.numpy(), w.numpy(), W, fmt, None))
+    fg.check_device_status()
