@@ -224,3 +224,21 @@ def test_quantizing_inside_leaves_the_same_bits(dev, fmt):
             if m not in (0, M // 2):
                 assert torch.equal(got[m], clean[m])
     fg.check_device_status()
+
+
+@pytest.mark.parametrize("fmt", [F32, UE8M0])
+def test_offsets_past_32_bits(dev, fmt):
+    """An output of more than 2^31 elements, added to in place: the rows on both
+    sides of the border and the last ones."""
+    M, N, K = 65800, 32768, 128
+    X = workloads.activations((M, K), "normal", seed=1)
+    Wq, Ws = fg.quant_weight(workloads.weights((N, K), seed=2).to(dev), fmt)
+    b = torch.randn(N, generator=torch.Generator().manual_seed(3))
+    Y = torch.full((M, N), 0.75, dtype=torch.bfloat16, device=dev)
+    fg.linear_epilogue(X.to(dev), Wq, Ws, fmt, bias=b.to(dev), act="silu", residual=Y, Y=Y)
+    fg.check_device_status()
+    rows = np.array([0, 32767, 32768, 65535, 65536, 65537, M - 1])
+    for r in rows:
+        one = X[r:r + 1]
+        y, tol = reference(one, Wq, Ws, fmt, b, "silu", torch.full((1, N), 0.75, dtype=torch.bfloat16))
+        check(Y[int(r):int(r) + 1], y, tol, f"row {r}")
