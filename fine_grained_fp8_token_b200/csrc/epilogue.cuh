@@ -191,21 +191,39 @@ __device__ __forceinline__ void staged_epilogue(const Put& put, uint8_t* slot, i
   }
 }
 
-// The same for a thread that has 128 columns of its own row m in registers
-// (accumulators as fp32 bits), where no shared memory is free: 32 columns a
-// step, whose residuals are in flight together.
-__device__ __forceinline__ void row_epilogue(const uint32_t (&acc)[128], const EpiArgs& e, __nv_bfloat16* Y, int N,
-                                             int m, int n0) {
-  const __nv_bfloat16* from = e.residual == nullptr ? nullptr : e.residual + static_cast<uint64_t>(m) * e.ld_r + n0;
-  __nv_bfloat16* to = Y + static_cast<uint64_t>(m) * N + n0;
+// The same for a warp whose lanes have 128 columns each of their own row in
+// registers (accumulators as fp32 bits), with a smaller slot (2 KB): the
+// arithmetic stays with the row's lane, and the residual and the output pass
+// through the slot as bf16, 32 columns a step, so that four neighbouring lanes
+// move 64 bytes of a row.  Lanes that read and wrote their own rows, 16 bytes
+// at a time, held up the next tile's operands in the same memory (4096 x 14336
+// x 4096: with a residual 231 us, through the slot 204; bias, gelu and residual
+// 235 and 216; none of them 200 and 194).  The residual alone through the slot
+// left half of that, and reading it a step ahead spilled registers.
+__device__ __forceinline__ void row_epilogue(const uint32_t (&acc)[128], uint8_t* slot, int lane, const EpiArgs& e,
+                                             __nv_bfloat16* Y, int N, int m0, int row_end, int n0) {
+  const int q = lane & 3, r0 = lane >> 2;    // 16-byte chunk q of rows r0 + 8 i
+  auto chunk = [&](int r, int c) { return reinterpret_cast<uint4*>(slot + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); };
 #pragma unroll
   for (int j = 0; j < 128; j += 32) {
-    uint4 res[4];
+    uint4 own[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) res[i] = make_uint4(0, 0, 0, 0);
-    if (from != nullptr) {
+    for (int i = 0; i < 4; ++i) own[i] = make_uint4(0, 0, 0, 0);
+    if (e.residual != nullptr) {
+      uint4 res[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) res[i] = *reinterpret_cast<const uint4*>(from + j + 8 * i);
+      for (int i = 0; i < 4; ++i) {
+        const int m = m0 + r0 + 8 * i;
+        res[i] = make_uint4(0, 0, 0, 0);
+        if (m < row_end)
+          res[i] = *reinterpret_cast<const uint4*>(e.residual + static_cast<uint64_t>(m) * e.ld_r + n0 + j + 8 * q);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *chunk(r0 + 8 * i, q) = res[i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) own[i] = *chunk(lane, i);
+      __syncwarp();
     }
     float x[32];
 #pragma unroll
@@ -217,7 +235,15 @@ __device__ __forceinline__ void row_epilogue(const uint32_t (&acc)[128], const E
     }
     apply_act_n(x, e.act);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(to + j + 8 * i) = add_round8(x + 8 * i, res[i]);
+    for (int i = 0; i < 4; ++i) *chunk(lane, i) = add_round8(x + 8 * i, own[i]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = m0 + r0 + 8 * i;
+      const uint4 v = *chunk(r0 + 8 * i, q);
+      if (m < row_end) *reinterpret_cast<uint4*>(Y + static_cast<uint64_t>(m) * N + n0 + j + 8 * q) = v;
+    }
+    __syncwarp();                            // the slot may be written again
   }
 }
 

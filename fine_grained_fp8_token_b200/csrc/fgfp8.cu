@@ -273,7 +273,7 @@ template <int BN, bool kGrouped, bool kEpi = false>
 fgfp8_status launch_gemm_mx(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq, const void* Ws,
                             void* Y, int64_t M, int64_t N, int64_t K, const int32_t* offs, int E, int64_t b_rows,
                             cudaStream_t stream, int dev, int sm_count, int early, int cap, int withhold_kb = -1, const fgfp8::EpiArgs& epi = {}) {
-  using C = fgfp8::MxCfg<BN>;
+  using C = fgfp8::MxCfg<BN, kEpi>;
   CUtensorMap mA, mB, mBh;
   fgfp8_status st = make_map_u8_sw128(&mA, Xq, static_cast<uint64_t>(M), static_cast<uint64_t>(K),
                                       static_cast<uint64_t>(K), 128, dev);

@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(GemmCfg<BN, CW>::kThreads, 1)
 // [0, 256).  Scale factors follow, two slots of 4 columns for A and BN / 32
 // for B.
 // ---------------------------------------------------------------------------
-template <int BN>
+template <int BN, bool kEpi = false>
 struct MxCfg {
   static constexpr int kBM = 128, kBN = BN, kBK = 128;
   static constexpr int kEpiWarps = 4 * (BN / 128);                 // one warp per 32 rows x 128 columns
@@ -790,8 +790,10 @@ struct MxCfg {
   static constexpr uint32_t kSfCol = kNumAcc * BN;                // scale factors after the accumulators
   static constexpr uint32_t kSfColsPerSlot = 4 + BN / 32;         // A: 4 columns, B: BN/32 columns
   static constexpr size_t kBarrierBytes = 256;
+  static constexpr uint32_t kSlotBytes = 2048;                    // epilogue: 32 rows x 32 bf16 per warp
+  static constexpr size_t kSlotArea = kEpi ? static_cast<size_t>(kEpiWarps) * kSlotBytes : 0;
   static constexpr size_t kSmemBytes = 1024 + kStages * static_cast<size_t>(kStageBytes) +
-                                       kSfSlots * static_cast<size_t>(kSfABytes + kSfBBytes) + kBarrierBytes;
+                                       kSfSlots * static_cast<size_t>(kSfABytes + kSfBBytes) + kSlotArea + kBarrierBytes;
 };
 
 template <int BN, bool kGrouped, bool kEpi = false>
@@ -801,7 +803,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::kThreads, 1)
                    const uint8_t* __restrict__ Ws, __nv_bfloat16* __restrict__ Y, int M, int N, int K,
                    const int32_t* __restrict__ group_offs, int E, int cap, int num_tiles, int num_full,
                    int early_b, int withhold_kb, int group_m, const __grid_constant__ EpiArgs epi) {
-  using C = MxCfg<BN>;
+  using C = MxCfg<BN, kEpi>;
   static_assert(!kEpi || !kGrouped, "bias, activation and residual: dense output only");
   constexpr bool kHalfTiles = !kGrouped && BN == 256;
   static_assert(C::kSfCol + C::kSfSlots * C::kSfColsPerSlot <= C::kTmemCols, "TMEM columns");
@@ -812,7 +814,8 @@ __global__ void __launch_bounds__(MxCfg<BN>::kThreads, 1)
   uint8_t* sB = sA + C::kStages * C::kABytes;
   uint8_t* sSfA = sB + C::kStages * C::kBBytes;
   uint8_t* sSfB = sSfA + C::kSfSlots * C::kSfABytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sSfB + C::kSfSlots * C::kSfBBytes);
+  uint8_t* sStg = sSfB + C::kSfSlots * C::kSfBBytes;  // epilogue slots
+  uint64_t* full = reinterpret_cast<uint64_t*>(sStg + C::kSlotArea);
   uint64_t* empty = full + C::kStages;
   uint64_t* tfull = empty + C::kStages;
   uint64_t* tempty = tfull + 2;
@@ -1134,7 +1137,7 @@ __global__ void __launch_bounds__(MxCfg<BN>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[tb]);
       if constexpr (kEpi) {
-        if (m < row_end) row_epilogue(p, epi, Y, N, m, n0 + col0);
+        row_epilogue(p, sStg + ew * C::kSlotBytes, lane, epi, Y, N, m0 + quad * 32, row_end, n0 + col0);
       } else if (m < row_end) {
 #pragma unroll
         for (int j = 0; j < 128; j += 8) {
