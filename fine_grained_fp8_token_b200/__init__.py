@@ -433,12 +433,10 @@ def _matrix(t, where: str, name: str, dtype, dev: int) -> int:
     if t.dtype is not dtype or t.dim() != 2 or t.get_device() != dev:
         _refuse(where, f"{name} must be a {dtype} matrix on device {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
     R, C = t.shape
-    if R <= 1:
-        return C                  # the stride of a single row says nothing
     ld, unit = t.stride()
-    if unit != 1 and C > 1:
+    if unit != 1 and C > 1 and R > 0:
         _refuse(where, f"{name} must have unit stride along its rows")
-    return ld
+    return ld if R > 1 else C     # the row stride of a single row says nothing
 
 
 def _dense(t, where: str, name: str, dtypes, shape, dev: int) -> None:
