@@ -817,10 +817,14 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
     // One meeting of the ranks: each thread's partial sums x of its row for
     // kRedTok tokens, `count` of them real, go to the tokens' owners, token q
     // to rank q % S, slot q / S; back come the sums over the ranks, added in
-    // rank order, of this rank's tokens in their slots.
+    // rank order, of this rank's tokens in their slots.  A meeting is counted
+    // before the waits that may expire: the cluster's first phase, which every
+    // thread arrives at once, is waited for at the first meeting, or, where
+    // none was begun (meets == 0), at the role's end, and never twice.
     auto meet = [&](float (&x)[C::kTiles][C::kRedTok], int count) {
-      if (meets == 0) cluster_wait();                                // the others' barriers exist
-      if (meets > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_empty[grp], (meets - 1) & 1u))) {
+      const uint32_t before = meets++;
+      if (before == 0) cluster_wait();                               // the others' barriers exist
+      if (before > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_empty[grp], (before - 1) & 1u))) {
         expired();
         return;
       }
@@ -834,7 +838,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       }
       __syncwarp();
       if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_full[grp]), lane));
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_full[grp], meets & 1u))) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&red_full[grp], before & 1u))) {
         expired();
         return;
       }
@@ -854,7 +858,6 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       }
       __syncwarp();
       if (lane < S) mbar_arrive_cluster(map_to_rank(smem_u32(&red_empty[grp]), lane));
-      ++meets;
     };
 
     // Output rows (Linear, Down): this rank's tokens of meeting c, all in
