@@ -788,6 +788,15 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
       }
       it = it_end;
     }
+    if constexpr (!kBf16) {
+      // Every copy that this warp issued must land before the CTA may exit.
+      // The TMA warp waits for its own blocks only: behind an expired wait,
+      // with two MMA warps, this warp may have come further.
+      if (lane == 0)
+        for (uint32_t u = mine > static_cast<uint32_t>(C::kStages) ? mine - C::kStages : 0; u < mine; ++u)
+          if ((u % C::kStages) % C::kTokWarps == me && !mbar_wait(&full[u % C::kStages], (u / C::kStages) & 1u))
+            record_status(kDevTimeoutProducer);
+    }
   } else {
     // ================= promotion and epilogue: thread = weight row
     const int grp = C::kGroups == 1 ? 0 : warp >> 2, quad = warp & 3;

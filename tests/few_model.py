@@ -5,8 +5,9 @@ Every role is a generator that yields where it may be overtaken.  Waits on
 barriers look at the parity only, as the hardware does, and the model checks
 that the phase behind the parity is the one that was meant; that no scale slot
 is overwritten before every promotion warp has read it; that the stuck roles of
-a launch with a withheld tile all come to an end; and that each thread waits for
-each phase of the cluster's barrier exactly once.
+a launch with a withheld tile all come to an end; that each thread waits for
+each phase of the cluster's barrier exactly once; and that every tile copy has
+been waited for by the time its CTA may exit.
 """
 import random
 
@@ -62,15 +63,16 @@ class Rank:
         self.red_empty = [Bar(warps * S) for _ in range(2)]
         self.values = [None] * c["slots"]             # the block whose scales a slot holds
         self.queue = [[] for _ in range(c["mma_warps"])]
+        self.copies, self.seen = set(), set()         # (block, role) requested; waited for at the end
         self.expired = 0
         self.left = 0                                 # roles that have not reached the CTA's last barrier
 
 
-def run(c, work, S=1, meetings=0, withhold=None, seed=0, patience=None, count_first=True):
+def run(c, work, S=1, meetings=0, withhold=None, seed=0, patience=None, count_first=True, wait_copies=True):
     """One launch of a cluster of S ranks.  work[r]: K blocks of rank r's
     segments.  After the last segment the promotion warps meet `meetings` times.
-    withhold: rank 0's weight tile that is never requested.  count_first:
-    False plants the form without that care.  Returns how many
+    withhold: rank 0's weight tile that is never requested.  count_first,
+    wait_copies: False plants the form without that care.  Returns how many
     waits expired."""
     rng = random.Random(seed)
     ranks = [Rank(c, S, work[r]) for r in range(S)]
@@ -108,6 +110,8 @@ def run(c, work, S=1, meetings=0, withhold=None, seed=0, patience=None, count_fi
                 yield from cluster.wait((r, name))
             cluster.arrive((r, name))
             yield from cluster.wait((r, name))
+        missing = k.copies - k.seen
+        assert not missing, f"copies {sorted(missing)[:3]} may land after the CTA's exit"
 
     def tma(r):
         k, total, it = ranks[r], sum(work[r]), 0
@@ -115,24 +119,37 @@ def run(c, work, S=1, meetings=0, withhold=None, seed=0, patience=None, count_fi
             if not (yield from stage_free(k, it)):
                 break
             if not (r == 0 and it == withhold):
+                k.copies.add((it, "tma"))
                 k.full[it % stages].arrive()
             it += 1
             yield
         for u in range(max(0, it - stages), it):
             yield from bounded(k.full[u % stages], u // stages, k)
+        # the wait for a block's barrier is one for both its copies; blocks before the last ring were consumed
+        k.seen |= {(u, n) for u in range(it) for n in ("tma", "tok")}
         yield from leave(r, "tma", False)
 
     def tok(r, w):
-        k, total = ranks[r], sum(work[r])
+        k, total, it, ok = ranks[r], sum(work[r]), 0, True
         own = [u for u in range(total) if (u % stages) % tok_warps == w]
+        done = []
         for u in own:
             if not (yield from stage_free(k, u)):
                 break
             k.values[u % slots] = u
+            if c["copies"]:
+                k.copies.add((u, "tok"))
             yield
             k.full[u % stages].arrive()
             k.sc[u % slots].arrive()
+            done.append(u)
             yield
+        if wait_copies and c["copies"]:
+            end = own[len(done)] if len(done) < len(own) else total
+            for u in done:
+                if u >= end - stages:
+                    yield from bounded(k.full[u % stages], u // stages, k)
+            k.seen |= {(u, "tok") for u in done}
         yield from leave(r, f"tok{w}", False)
 
     def pairs_of(r):

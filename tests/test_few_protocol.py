@@ -88,3 +88,12 @@ def test_the_model_sees_broken_pipelines():
     assert caught(dict(WIDE, stages=3), 40) > 0
     assert caught(dict(WIDE, mma_warps=1, stages=8, slots=9), 40) > 0
     assert caught(WIDE, 200) == 0
+
+
+def test_the_model_sees_copies_that_nobody_waited_for():
+    """Two MMA warps: behind a withheld tile the other warp's blocks go on, and
+    with them the token rows' copies, past the last tile that the TMA warp
+    waits for.  The token warps wait for their own."""
+    for c in (WIDE, dict(WIDE, stages=8)):
+        assert caught(c, 40, withhold=4, patience=400, wait_copies=False) > 0
+        assert caught(c, 40, withhold=4, patience=400) == 0
