@@ -61,6 +61,9 @@ SIGNATURES = {
     "fgfp8_gather_cols": (_INT, [_P, _I64, _I64, _I64, _P, _P]),
     "fgfp8_selftest_expired_wait": (_INT, [_P]),
     "fgfp8_selftest_gemm_timeout": (_INT, [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _INT, _I64, _P]),
+    "fgfp8_selftest_few_timeout": (_INT, [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _INT, _I64, _P]),
+    "fgfp8_selftest_moe_timeout": (_INT, [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64,
+                                          _INT, _INT, _I64, _P]),
 }
 
 _lock = threading.Lock()
@@ -136,6 +139,8 @@ fgfp8_check_device_status = _raw("fgfp8_check_device_status")
 fgfp8_gather_cols = _raw("fgfp8_gather_cols")
 fgfp8_selftest_expired_wait = _raw("fgfp8_selftest_expired_wait")
 fgfp8_selftest_gemm_timeout = _raw("fgfp8_selftest_gemm_timeout")
+fgfp8_selftest_few_timeout = _raw("fgfp8_selftest_few_timeout")
+fgfp8_selftest_moe_timeout = _raw("fgfp8_selftest_moe_timeout")
 
 
 def fgfp8_last_error_string() -> str:

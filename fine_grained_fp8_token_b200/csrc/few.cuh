@@ -84,6 +84,7 @@ struct FewArgs {
   EpiArgs epi;
   int lgS;                          // log2 of the cluster size S: ranks that split K
   int early;                        // weights may be requested before the wait for the preceding grid
+  int withhold = -1;                // self-tests: CTA 0 never requests its withhold-th weight tile
 };
 
 template <int MODE, int NT>
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(FewCfg<MODE, NT>::kThreads, FewCfg<MODE, NT>::
             ok = false;
             break;
           }
+          if (blockIdx.x == 0 && static_cast<int>(it) == p.withhold) continue;
           mbar_arrive_expect_tx(&full[s], C::kABytes);
           tma_load_2d(sA + s * C::kABytes, &tmW, &full[s], kb * 128, row);
         }

@@ -786,8 +786,9 @@ fgfp8::EpiArgs make_epilogue(const void* bias, int bias_type, int act, const voi
 template <bool kBf16>
 fgfp8_status few_linear(const void* src, int64_t ld_src, const void* Xs, int64_t ld_s, const uint8_t* Wq,
                         const void* Ws, void* Y, int64_t M, int64_t N, int64_t K, int fmt, const fgfp8::EpiArgs& epi,
-                        cudaStream_t stream, int dev, int sm_count, int early) {
+                        cudaStream_t stream, int dev, int sm_count, int early, int withhold = -1) {
   fgfp8::FewArgs a{};
+  a.withhold = withhold;
   a.src = src;
   a.ld_src = static_cast<uint64_t>(ld_src);
   a.src_scale = Xs;
@@ -874,7 +875,7 @@ template <int NT, bool kBf16>
 fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const float* weights, const uint8_t* W13q,
                         const void* W13s, const uint8_t* W2q, const void* W2s, const fgfp8::EpiArgs& epi, void* Y,
                         uint8_t* ws, int64_t T, int64_t topk, int64_t E, int64_t K, int64_t I, int fmt,
-                        cudaStream_t s, int dev, int sms) {
+                        cudaStream_t s, int dev, int sms, const int (&withhold)[2]) {
   fgfp8::FewArgs a{};
   a.fmt = fmt;
   a.T = static_cast<int>(T);
@@ -907,6 +908,7 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
   a.Ws = W13s;
   a.KB = KB13;
   a.NB = 2 * KB2;
+  a.withhold = withhold[0];
   st = launch_few<fgfp8::kFewGateUp, NT, kBf16>(W13q, static_cast<uint64_t>(E) * 2 * I, static_cast<uint64_t>(T), a,
                                                 most * KB2, lg13, s, dev, sms, "expert gate/up launch");
   if (st != FGFP8_OK) return st;
@@ -920,8 +922,52 @@ fgfp8_status launch_moe(const void* X, int64_t ldx, const int32_t* ids, const fl
   a.Y = reinterpret_cast<__nv_bfloat16*>(Y);
   a.N = static_cast<int>(K);
   a.epi = epi;
+  a.withhold = withhold[1];
   return launch_few<fgfp8::kFewDown, NT, false>(W2q, static_cast<uint64_t>(E) * K, static_cast<uint64_t>(T) * topk, a,
                                                 a.NB, lg2, s, dev, sms, "expert down launch");
+}
+
+// The expert layer; withhold: per kernel, the weight tile that CTA 0 never
+// requests (self-tests), or -1.
+fgfp8_status moe_decode_impl(const void* X, int64_t ldx, const int32_t* ids, const float* weights, const uint8_t* W13q,
+                             const void* W13s, const uint8_t* W2q, const void* W2s, const void* residual, int64_t ld_r,
+                             void* Y, void* workspace, int64_t workspace_bytes, int64_t T, int64_t topk, int64_t E,
+                             int64_t K, int64_t I, int fmt, void* stream, const int (&withhold)[2]) {
+  fgfp8_status st = check_fmt(fmt);
+  if (st != FGFP8_OK) return st;
+  if (E < 0 || ldx < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
+  st = check_moe_sizes(T, topk, K, I);
+  if (st != FGFP8_OK) return st;
+  if (E < 1 || E > fgfp8::kFewMaxExperts) return fail(FGFP8_ERR_SHAPE, "E must be in [1, 512]");
+  if (E * 2 * I >= (int64_t(1) << 31) || E * K >= (int64_t(1) << 31))
+    return fail(FGFP8_ERR_SHAPE, "E*2*I and E*K must be < 2^31");
+  if (ldx < K) return fail(FGFP8_ERR_SHAPE, "ldx must be >= K");
+  if (T == 0) return ok();
+  if (!X || !ids || !weights || !W13q || !W13s || !W2q || !W2s || !Y || !workspace)
+    return fail(FGFP8_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!aligned(X, 16) || ldx % 8 != 0) return fail(FGFP8_ERR_ALIGN, "X must be 16-byte aligned with ldx % 8 == 0");
+  if (!aligned(W13q, 16) || !aligned(W2q, 16) || !aligned(Y, 16))
+    return fail(FGFP8_ERR_ALIGN, "W13q, W2q and Y must be 16-byte aligned");
+  if (!aligned(ids, 4) || !aligned(weights, 4)) return fail(FGFP8_ERR_ALIGN, "ids and weights must be 4-byte aligned");
+  if (fmt == FGFP8_SCALE_F32 && (!aligned(W13s, 4) || !aligned(W2s, 4)))
+    return fail(FGFP8_ERR_ALIGN, "fp32 W13s and W2s must be 4-byte aligned");
+  if (!aligned(workspace, 256)) return fail(FGFP8_ERR_ALIGN, "workspace must be 256-byte aligned");
+  if (workspace_bytes < MoeWorkspace(T, topk, K, I).bytes)
+    return fail(FGFP8_ERR_SHAPE, "workspace_bytes is below fgfp8_moe_workspace_bytes");
+  st = check_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r, Y, T, K);
+  if (st != FGFP8_OK) return st;
+  int dev;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != FGFP8_OK) return st;
+  const fgfp8::EpiArgs epi = make_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T <= FGFP8_MOE_FUSED_TOKENS)
+    return launch_moe<16, true>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
+                                info.sm_count, withhold);
+  return launch_moe<64, false>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
+                               info.sm_count, withhold);
 }
 
 template <bool kSigmoid, typename In>
@@ -1330,41 +1376,8 @@ fgfp8_status fgfp8_moe_decode(const void* X, int64_t ldx, const int32_t* ids, co
                               const uint8_t* W13q, const void* W13s, const uint8_t* W2q, const void* W2s,
                               const void* residual, int64_t ld_r, void* Y, void* workspace, int64_t workspace_bytes,
                               int64_t T, int64_t topk, int64_t E, int64_t K, int64_t I, int fmt, void* stream) {
-  fgfp8_status st = check_fmt(fmt);
-  if (st != FGFP8_OK) return st;
-  if (E < 0 || ldx < 0) return fail(FGFP8_ERR_INVALID_ARG, "negative size");
-  st = check_moe_sizes(T, topk, K, I);
-  if (st != FGFP8_OK) return st;
-  if (E < 1 || E > fgfp8::kFewMaxExperts) return fail(FGFP8_ERR_SHAPE, "E must be in [1, 512]");
-  if (E * 2 * I >= (int64_t(1) << 31) || E * K >= (int64_t(1) << 31))
-    return fail(FGFP8_ERR_SHAPE, "E*2*I and E*K must be < 2^31");
-  if (ldx < K) return fail(FGFP8_ERR_SHAPE, "ldx must be >= K");
-  if (T == 0) return ok();
-  if (!X || !ids || !weights || !W13q || !W13s || !W2q || !W2s || !Y || !workspace)
-    return fail(FGFP8_ERR_INVALID_ARG, "a required pointer is NULL");
-  if (!aligned(X, 16) || ldx % 8 != 0) return fail(FGFP8_ERR_ALIGN, "X must be 16-byte aligned with ldx % 8 == 0");
-  if (!aligned(W13q, 16) || !aligned(W2q, 16) || !aligned(Y, 16))
-    return fail(FGFP8_ERR_ALIGN, "W13q, W2q and Y must be 16-byte aligned");
-  if (!aligned(ids, 4) || !aligned(weights, 4)) return fail(FGFP8_ERR_ALIGN, "ids and weights must be 4-byte aligned");
-  if (fmt == FGFP8_SCALE_F32 && (!aligned(W13s, 4) || !aligned(W2s, 4)))
-    return fail(FGFP8_ERR_ALIGN, "fp32 W13s and W2s must be 4-byte aligned");
-  if (!aligned(workspace, 256)) return fail(FGFP8_ERR_ALIGN, "workspace must be 256-byte aligned");
-  if (workspace_bytes < MoeWorkspace(T, topk, K, I).bytes)
-    return fail(FGFP8_ERR_SHAPE, "workspace_bytes is below fgfp8_moe_workspace_bytes");
-  st = check_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r, Y, T, K);
-  if (st != FGFP8_OK) return st;
-  int dev;
-  DeviceInfo info;
-  st = current_device(&dev, &info);
-  if (st != FGFP8_OK) return st;
-  const fgfp8::EpiArgs epi = make_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, residual, ld_r);
-  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (T <= FGFP8_MOE_FUSED_TOKENS)
-    return launch_moe<16, true>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
-                          info.sm_count);
-  return launch_moe<64, false>(X, ldx, ids, weights, W13q, W13s, W2q, W2s, epi, Y, ws, T, topk, E, K, I, fmt, s, dev,
-                        info.sm_count);
+  return moe_decode_impl(X, ldx, ids, weights, W13q, W13s, W2q, W2s, residual, ld_r, Y, workspace, workspace_bytes, T,
+                         topk, E, K, I, fmt, stream, {-1, -1});
 }
 
 fgfp8_status fgfp8_selftest_expired_wait(void* stream) {
@@ -1394,6 +1407,34 @@ fgfp8_status fgfp8_selftest_gemm_timeout(const uint8_t* Xq, const void* Xs, int6
     return launch_gemm_mx<256, false>(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, nullptr, 1, N, s, dev, info.sm_count, 0, 0, kb);
   return launch_gemm<256, 128, 0, false>(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, nullptr, 1, N, s, dev, info.sm_count, 0, 0,
                                          nullptr, nullptr, 0, kb);
+}
+
+fgfp8_status fgfp8_selftest_few_timeout(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq,
+                                        const void* Ws, void* Y, int64_t M, int64_t N, int64_t K, int fmt,
+                                        int64_t withhold, void* stream) {
+  fgfp8_status st = check_gemm_common(Xq, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt);
+  if (st != FGFP8_OK) return st;
+  if (M < 1 || M > fgfp8::kFewMaxTokens) return fail(FGFP8_ERR_SHAPE, "the self-test runs the few-token kernel: 1 <= M <= 64");
+  if (withhold < 0 || withhold >= K / 128) return fail(FGFP8_ERR_INVALID_ARG, "withhold must be in [0, K/128)");
+  int dev;
+  DeviceInfo info;
+  st = current_device(&dev, &info);
+  if (st != FGFP8_OK) return st;
+  return few_linear<false>(Xq, K, Xs, ld_s, Wq, Ws, Y, M, N, K, fmt,
+                           make_epilogue(nullptr, FGFP8_BF16, FGFP8_ACT_NONE, nullptr, 0),
+                           reinterpret_cast<cudaStream_t>(stream), dev, info.sm_count, 0, static_cast<int>(withhold));
+}
+
+fgfp8_status fgfp8_selftest_moe_timeout(const void* X, int64_t ldx, const int32_t* ids, const float* weights,
+                                        const uint8_t* W13q, const void* W13s, const uint8_t* W2q, const void* W2s,
+                                        void* Y, void* workspace, int64_t workspace_bytes, int64_t T, int64_t topk,
+                                        int64_t E, int64_t K, int64_t I, int fmt, int kernel, int64_t withhold,
+                                        void* stream) {
+  if (kernel != 0 && kernel != 1) return fail(FGFP8_ERR_INVALID_ARG, "kernel must be 0 (gate/up) or 1 (down)");
+  if (withhold < 0 || withhold >= (int64_t(1) << 31)) return fail(FGFP8_ERR_INVALID_ARG, "withhold must be in [0, 2^31)");
+  const int tile = static_cast<int>(withhold);
+  return moe_decode_impl(X, ldx, ids, weights, W13q, W13s, W2q, W2s, nullptr, 0, Y, workspace, workspace_bytes, T, topk,
+                         E, K, I, fmt, stream, {kernel == 0 ? tile : -1, kernel == 1 ? tile : -1});
 }
 
 fgfp8_status fgfp8_check_device_status(void* stream) {

@@ -504,6 +504,29 @@ fgfp8_status fgfp8_selftest_gemm_timeout(const uint8_t* Xq, const void* Xs, int6
                                          int64_t withhold_kb, void* stream);
 
 /*
+ * The same for the few-token kernels, whose ranks meet in a cluster: CTA 0
+ * never requests the withhold-th of the weight tiles that it would request,
+ * counted from 0 (one per 128 of K, in its own order).  Its roles give up as
+ * above, the other ranks of its cluster when their meeting's wait expires, and
+ * all of them leave the cluster together; the launch ends within seconds,
+ * fgfp8_check_device_status returns FGFP8_ERR_TIMEOUT, the context stays
+ * usable, and what that cluster would have written is left unspecified (gate/up:
+ * all of Y).  A tile beyond CTA 0's share withholds nothing.
+ *   few  the linear layer from codes (fgfp8_gemm_epilogue without bias,
+ *        activation and residual) at 1 <= M <= 64, 0 <= withhold < K/128.
+ *   moe  fgfp8_moe_decode without a residual; kernel 0: gate/up, 1: down.
+ */
+fgfp8_status fgfp8_selftest_few_timeout(const uint8_t* Xq, const void* Xs, int64_t ld_s, const uint8_t* Wq,
+                                        const void* Ws, void* Y, int64_t M, int64_t N, int64_t K, int fmt,
+                                        int64_t withhold, void* stream);
+
+fgfp8_status fgfp8_selftest_moe_timeout(const void* X, int64_t ldx, const int32_t* ids, const float* weights,
+                                        const uint8_t* W13q, const void* W13s, const uint8_t* W2q, const void* W2s,
+                                        void* Y, void* workspace, int64_t workspace_bytes, int64_t T, int64_t topk,
+                                        int64_t E, int64_t K, int64_t I, int fmt, int kernel, int64_t withhold,
+                                        void* stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the device status word that
  * the kernels set when they give up.  It returns FGFP8_OK,
  * FGFP8_ERR_TIMEOUT (a barrier wait ran past its one-second limit),
