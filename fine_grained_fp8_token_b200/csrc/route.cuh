@@ -287,22 +287,26 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_topk_kernel(const Rout
     uint32_t first, second;
     group_top2(keys, p, lane, 0u, first, second);
     const float a = value_of(first), b = value_of(second);
-    float score = a;
+    float score = a, slack = 0.0f;
     if (kSigmoid && first != 0u) {
       score = biased ? a : sigmoid_key(a);
-      if (second != 0u) score += biased ? b : sigmoid_key(b);
+      slack = key_slack(score);
+      if (second != 0u) {
+        const float k = biased ? b : sigmoid_key(b);
+        // the keys' slacks, as the two may cancel; twice the keys' errors, they
+        // leave room for the rounding of the sum and of score -+ slack
+        slack += key_slack(k);
+        score += k;
+      }
     }
     kept = best_groups(score, p, lane);
     if constexpr (kSigmoid) {
-      // the worst group that competes against the best that does not
+      // the worst group that competes at its lowest against the best that does
+      // not at its highest; an infinite or NaN bound is not clear
       const bool in = (kept >> lane) & 1u;
-      const uint32_t lo = ~__reduce_max_sync(0xFFFFFFFFu, in ? ~order_of(score) : 0u);
-      const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, !in && lane < p.n_group ? order_of(score) : 0u);
-      if (hi != 0u) {
-        const float l = value_of(lo), h = value_of(hi);
-        // each score is the sum of two keys
-        if (!(l - h > 2.0f * (key_slack(l) + key_slack(h)))) kept = exact_groups<EPL>(p, row, s_keys[w]);
-      }
+      const uint32_t lo = ~__reduce_max_sync(0xFFFFFFFFu, in ? ~order_of(score - slack) : 0u);
+      const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, !in && lane < p.n_group ? order_of(score + slack) : 0u);
+      if (hi != 0u && !(value_of(lo) > value_of(hi))) kept = exact_groups<EPL>(p, row, s_keys[w]);
     }
     const int per = p.per.d;
     int g = p.per.div(e0), left = (g + 1) * per - e0;             // experts left in this lane's group
