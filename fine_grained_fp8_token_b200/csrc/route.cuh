@@ -66,7 +66,11 @@ __device__ __forceinline__ float value_of(uint32_t o) {
   return o == 0u ? -INFINITY : __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
-__device__ __forceinline__ float sigmoid_f32(float z) { return __fdiv_rn(1.0f, 1.0f + expf(-z)); }
+// From exp(-|z|), which keeps results below fp32's normal numbers and does not overflow.
+__device__ __forceinline__ float sigmoid_f32(float z) {
+  const float e = expf(-fabsf(z));
+  return __fdiv_rn(z < 0.0f ? e : 1.0f, 1.0f + e);
+}
 
 // sigma(z) for the 32-bit keys, from the hardware's exponential and division.
 // With r the relative error of exp(-z), 2^-22 + |z| 2^-24, sigma is off by
