@@ -18,10 +18,14 @@
 // warp-wide redux over the lanes' heads and a ballot, whose lowest lane is the
 // lowest index; the winner drops its head.  Which of its experts that was is
 // found for all slots together at the end.  The kernel is bound by issuing
-// instructions (about 15 a round and 100 around them), not by its 4 E bytes
-// per token: 8192 tokens x 256 experts in 8 groups with a bias 16 us, 20011 x
-// 160 softmax 11 us, one token 3.7 us (selecting with a lane's maximum and
-// 64-bit shuffles took 49, 27 and 14).
+// instructions, not by its 4 E bytes per token.  Counted with 8 experts a lane,
+// per token: 30 a round, and around the rounds 300 (fp32 softmax) to 360 (bf16),
+// 570 with biased sigmoids and 940 with groups on top (the keys staged in shared
+// memory and scanned).  20011 tokens x 160 softmax, 6 of them, are 545 x 20011 =
+// 10.9 M, 9.4 us of the SMs' issue slots at 1.965 GHz, and take 11.5 us; 8192 x
+// 256 in 8 groups with a bias 1200 x 8192 = 9.8 M and 16 us; one token 3.7 us
+// (selecting with a lane's maximum and 64-bit shuffles took 49, 27 and 14 us for
+// the second, the first and the last).
 //
 // sigma(z) + bias is defined in 64 bits.  The warp forms it in 32 and looks at
 // the gaps its decisions rest on; where one is within the 32-bit error, it

@@ -252,6 +252,11 @@ fgfp8_status fgfp8_grouped_linear(const void* X, int64_t ldx, uint8_t* Xq, void*
  * fgfp8_linear_epilogue neither reads nor writes Xq and Xs when M <=
  * FGFP8_FUSED_QUANT_TOKENS: it then quantizes X inside the GEMM, and Xq and
  * Xs may be NULL.  Within act, NaN stays NaN.
+ * With nothing asked for the result is fgfp8_linear's up to the order of sums.
+ * Up to 64 tokens this call is the faster one, as it splits K where there are
+ * few weight blocks (4096 x 14336, 1 to 64 tokens: 15 to 23 us, fgfp8_linear 45
+ * to 51; 18432 x 7168: 24 to 28 and 27 to 31, the same at 8 tokens and UE8M0);
+ * above, fgfp8_linear is, by 1 to 11%.
  */
 #define FGFP8_FUSED_QUANT_TOKENS 8
 
