@@ -207,7 +207,7 @@ __device__ __forceinline__ void staged_epilogue(const Put& put, uint8_t* slot, i
 // move 64 bytes of a row.  Lanes that read and wrote their own rows, 16 bytes
 // at a time, held up the next tile's operands in the same memory (4096 x 14336
 // x 4096: with a residual 231 us, through the slot 204; bias, gelu and residual
-// 235 and 216; none of them 200 and 194).  The residual alone through the slot
+// 235 and 216, 222 with gelu's present fit; none of them 200 and 194).  The residual alone through the slot
 // left half of that, and reading it a step ahead spilled registers.
 __device__ __forceinline__ void row_epilogue(const uint32_t (&acc)[128], uint8_t* slot, int lane, const EpiArgs& e,
                                              __nv_bfloat16* Y, int N, int m0, int row_end, int n0) {

@@ -31,8 +31,8 @@
 //
 // Measured (one B200, back to back in a CUDA graph, weights read once at the
 // measured 6.57 TB/s as the floor): 1 token x 8 of 256 experts of 7168 x 2048
-// 70 us (floor 53.7), 7 tokens 353 (342), 64 tokens x 32 experts 257 (215);
-// linear 1 x 4096 x 4096 7.0 us (2.6), 37 x 18432 x 7168 28 us (20.4).  What
+// 71 us (floor 53.7), 7 tokens 355 (342), 64 tokens x 32 experts 257 (215);
+// linear 1 x 4096 x 4096 7.2 us (2.6), 37 x 18432 x 7168 28 us (20.4).  What
 // remains is the start (launch, routing, the first weights' latency: 5 to 8
 // us), the gate/up kernel's end (its last epilogues and the hand-over, 5 us),
 // and with few blocks the ranks' meeting (2 us).
