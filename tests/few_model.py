@@ -130,7 +130,7 @@ def run(c, work, S=1, meetings=0, withhold=None, seed=0, patience=None, count_fi
         yield from leave(r, "tma", False)
 
     def tok(r, w):
-        k, total, it, ok = ranks[r], sum(work[r]), 0, True
+        k, total = ranks[r], sum(work[r])
         own = [u for u in range(total) if (u % stages) % tok_warps == w]
         done = []
         for u in own:

@@ -5,14 +5,13 @@ FGFP8_ERR_TIMEOUT.  The other clusters' output is correct, and the next call on
 the same context is correct everywhere."""
 import time
 
-import numpy as np
 import pytest
 import torch
 
 import fine_grained_fp8_token_b200 as fg
 import oracle
 import workloads
-from parity import F32, UE8M0, assert_gemm_close, bits16, require_gpu, to_np, y_to_f64
+from parity import F32, UE8M0, assert_gemm_close, require_gpu, to_np, y_to_f64
 
 pytestmark = pytest.mark.gpu
 TIMEOUT = 6
